@@ -433,6 +433,173 @@ int ssm_scan_bwd_train(const void* x, const void* delta, const float* A, const v
 
 size_t ssm_scan_bwd_train_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t dstate, int flags);
 
+/*
+ * Gradient of ssm_causal_conv1d_fwd for the same inputs: with dout =
+ * dloss/dout and optionally dstate_out = dloss/dstate_out,
+ *   pre_t   = the convolution at token t (recomputed), dpre_t = dout_t silu'(pre_t)
+ *   dxx[p]  = sum_k weight[d,k] dpre[p + (width-1) - k] over the segment's tokens,
+ *             plus dstate_out where p is one of the last width-1 inputs
+ *   dweight[d,k] = sum_{b,t} dpre_t xx[t-(width-1)+k],  dbias[d] = sum_{b,t} dpre_t.
+ *
+ *   x, dout, dx : (batch, seqlen, dim) act dtype (required)
+ *   dstate_out  : (batch, dim, width-1) act dtype or NULL (zeros)
+ *   dweight     : (dim, width) fp32 (required)
+ *   dbias       : (dim) fp32, required when bias is given, else ignored
+ *   dstate_in   : (batch, dim, width-1) act dtype or NULL: the gradient of the
+ *                 carried-in inputs (of zeros where state_in is NULL)
+ * The sums over batch and tokens are taken in a fixed order: the same call
+ * gives the same bits.  With batch or seqlen 0, dweight and dbias are zeros.
+ * Workspace: ssm_causal_conv1d_bwd_workspace_bytes() (the workgroups' shares
+ * of dweight and dbias), or NULL for stream-ordered scratch.
+ */
+int ssm_causal_conv1d_bwd(const void* x, const float* weight, const float* bias, const void* state_in, int silu,
+                          const void* dout, const void* dstate_out, void* dx, float* dweight, float* dbias,
+                          void* dstate_in, int64_t batch, int64_t seqlen, int64_t dim, int64_t width,
+                          int act_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+size_t ssm_causal_conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t width);
+
+/* forms of the gated scan */
+enum ssm_gated_form {
+  SSM_GATED_LRU = 0,   /* two gates and a decay per channel */
+  SSM_GATED_UNIT = 1   /* one gate */
+};
+
+/*
+ * Gated linear recurrence, elementwise over channels: the recurrence of a
+ * block whose state is one value per channel and whose decay each token sets
+ * for itself.  For every batch row and channel, with h = h0 before token 0
+ * (zeros if h0 == NULL):
+ *
+ *   SSM_GATED_LRU :  a = exp(A[d] sigma(r[b,t,d])),
+ *                    h = a h + sqrt(1 - a^2) sigma(i[b,t,d]) x[b,t,d]
+ *   SSM_GATED_UNIT:  a = sigma(r[b,t,d]),
+ *                    h = a h + (1 - a) x[b,t,d]
+ *   y[b,t,d] = h;  h_final[b,d] = h after the last token.
+ *
+ * Where reset[b,t] is not 0, a is 0: the token starts a new sequence (h = the
+ * input's part alone), and nothing from before it, not even a NaN, is seen
+ * from it on.  Packed sequences set it at each first token.
+ *
+ *   x, r, i, y  : (batch, seqlen, dim) act dtype (i: SSM_GATED_LRU only, else NULL)
+ *   A           : (dim) fp32, <= 0 (a positive A gives NaN); SSM_GATED_LRU only, else NULL
+ *   reset       : (batch, seqlen) bytes or NULL (no resets)
+ *   h0, h_final : (batch, dim) fp32 or NULL; h_final may be h0
+ *   states      : NULL, or, for training, fp32 (ceil(seqlen/64), batch, dim):
+ *                 states[k] receives the state before token 64k (states[0] is
+ *                 h0), for ssm_gated_scan_bwd; ssm_gated_scan_states_bytes()
+ *   y           : required; must not overlap an input
+ * Workspace: ssm_gated_scan_workspace_bytes() (0 unless few rows of few
+ * channels make it split the sequence into chunks that run in parallel), or
+ * NULL for stream-ordered scratch.
+ */
+int ssm_gated_scan_fwd(const void* x, const void* r, const void* i, const float* A, const uint8_t* reset,
+                       const float* h0, void* y, float* h_final, float* states,
+                       int64_t batch, int64_t seqlen, int64_t dim, int form, int act_dtype,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace of ssm_gated_scan_fwd.  Depends on the current device. */
+size_t ssm_gated_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int act_dtype);
+
+/* Bytes of states: ceil(seqlen/64) * batch * dim * 4.  0 for empty sizes. */
+size_t ssm_gated_scan_states_bytes(int64_t batch, int64_t seqlen, int64_t dim);
+
+/*
+ * Gradient of ssm_gated_scan_fwd: of sum dout * y + sum dh_final * h_final with
+ * respect to x, r, i, A and h0, for the same inputs and form.  At a reset the
+ * token's r, its share of A and everything before it get none.  Where 1 - a^2
+ * is 0 (A = 0, or sigma(r) rounded to 0) the square root has no derivative and
+ * its share of dr and dA counts as 0.
+ *
+ *   states    : as ssm_gated_scan_fwd wrote them for these inputs, or NULL, in
+ *               which case a first pass over the sequence computes them into
+ *               the workspace.  States of other inputs give meaningless
+ *               gradients (no check is possible).
+ *   dout      : (batch, seqlen, dim) act dtype (required)
+ *   dh_final  : (batch, dim) fp32 or NULL (zeros)
+ *   dx, dr, di: (batch, seqlen, dim) act dtype (di: SSM_GATED_LRU only, else ignored)
+ *   dA        : (dim) fp32, SSM_GATED_LRU only, else ignored; summed in a fixed order
+ *   dh0       : (batch, dim) fp32 or NULL
+ * Outputs must not overlap inputs.  Workspace:
+ * ssm_gated_scan_bwd_workspace_bytes(), or NULL for stream-ordered scratch.
+ */
+int ssm_gated_scan_bwd(const void* x, const void* r, const void* i, const float* A, const uint8_t* reset,
+                       const float* h0, const float* states, const void* dout, const float* dh_final,
+                       void* dx, void* dr, void* di, float* dA, float* dh0,
+                       int64_t batch, int64_t seqlen, int64_t dim, int form, int act_dtype,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace of ssm_gated_scan_bwd (have_states: 1 with states, else 0).
+ * Depends on the current device. */
+size_t ssm_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int act_dtype, int have_states);
+
+/*
+ * One token of the gated scan (decoding): state is h, read and overwritten, y
+ * that token's output.
+ *   x, r, i, y : (batch, dim) act dtype (i: SSM_GATED_LRU only, else NULL)
+ *   A          : (dim) fp32; SSM_GATED_LRU only, else NULL
+ *   state      : (batch, dim) fp32 (required)
+ *   y          : required; must not overlap the state or an input
+ * No workspace.
+ */
+int ssm_gated_state_update(const void* x, const void* r, const void* i, const float* A, float* state, void* y,
+                           int64_t batch, int64_t dim, int form, int act_dtype, void* stream);
+
+/*
+ * What stands between two residual blocks, in one pass: the gate on the
+ * block's branch, the norm after the block, the residual scale, dropout, the
+ * residual sum, and the norm before the next block.  Per row, in fp32, each
+ * bracket left out where its pointer is NULL (dropout where p rounds to 0):
+ *
+ *   v   = y [* silu(z)]
+ *   n   = [v / sqrt(mean(v^2) + eps) * w_post]         (v without w_post)
+ *   R   = [residual +] [dropout]([scale *] n)
+ *   out = R / sqrt(mean(R^2) + eps) * w_pre
+ *
+ * Dropout drops element e (row-major over rows x dim) iff the 16-bit number
+ * u_e < q, q = p * 65536 rounded to the nearest whole number, and multiplies
+ * the kept ones by 65536 / (65536 - q).  u_e is the half e % 8 (low half
+ * first) of the four words of Philox4x32-10 (Salmon, Moraes, Dror, Shaw, SC
+ * 2011) with key rng[0] and counter (e / 8, rng[1]), 64-bit numbers low word
+ * first.  Nothing is stored: the gradient makes the same numbers again.  rng
+ * is read on the device when the kernel runs, so a captured graph takes the
+ * numbers that are there at each replay.
+ *
+ *   y, z, out          : (rows, dim) act dtype
+ *   residual, res_out  : (rows, dim) res dtype; res_out (R) may be residual
+ *   w_post, scale, w_pre : (dim) fp32
+ *   rng                : 2 x int64 on the device: seed, offset; required when p > 0
+ *   p                  : drop probability in [0, 1), eps > 0
+ *   out                : required with w_pre, NULL without
+ *   res_out            : required without w_pre, else may be NULL
+ * out is formed from R before R is rounded to res dtype.  dim up to 16384
+ * (SSM_ERR_UNSUPPORTED above).  No workspace.
+ */
+int ssm_block_norm_fwd(const void* y, const void* z, const void* residual, const float* w_post, const float* scale,
+                       const float* w_pre, const int64_t* rng, float p, float eps, void* res_out, void* out,
+                       int64_t rows, int64_t dim, int act_dtype, int res_dtype, void* stream);
+
+/*
+ * Gradient of ssm_block_norm_fwd: of sum dres * R + sum dout * out, for the same
+ * inputs (rng holding the forward's numbers).  Everything is recomputed from
+ * the forward's inputs.
+ *   dres       : (rows, dim) res dtype or NULL (zeros; required without w_pre)
+ *   dout       : (rows, dim) act dtype; given exactly when w_pre is
+ *   dy         : (rows, dim) act dtype (required)
+ *   dz, dresidual, dw_post, dscale, dw_pre : required when z, residual,
+ *                w_post, scale, w_pre are given, else ignored; the last three
+ *                (dim) fp32, summed over the rows in a fixed order
+ * Outputs must not overlap inputs.  Workspace:
+ * ssm_block_norm_bwd_workspace_bytes(), or NULL for stream-ordered scratch.
+ */
+int ssm_block_norm_bwd(const void* y, const void* z, const void* residual, const float* w_post, const float* scale,
+                       const float* w_pre, const int64_t* rng, float p, float eps, const void* dres,
+                       const void* dout, void* dy, void* dz, void* dresidual, float* dw_post, float* dscale,
+                       float* dw_pre, int64_t rows, int64_t dim, int act_dtype, int res_dtype,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+size_t ssm_block_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
+
 /* Static text for a status code (never NULL). */
 const char* ssm_status_string(int status);
 

@@ -1,4 +1,5 @@
-"""MI355X-native selective state-space scan (Mamba S6) and its Mamba-2 SSD form.
+"""MI355X-native selective state-space scan (Mamba S6), its Mamba-2 SSD form, the gated linear
+recurrence, and the convolution and block norm around them.
 
 Thin Python binding over the C ABI in ``include/ssm_mi355x.h`` (library
 ``libssm_mi355x.so`` built in-tree by ``build.py``).  The functions carry the
@@ -7,13 +8,27 @@ torch, and pass raw device pointers plus the current HIP stream.  All
 computation happens in the library's HIP kernels; there is no fallback.
 """
 from ._binding import (  # noqa: F401
+    SSM_GATED_LRU,
+    SSM_GATED_UNIT,
     SSM_SCAN_DELTA_PER_TOKEN,
     SSM_SCAN_EULER,
     SSM_SCAN_REVERSE,
     SSMError,
     library_path,
     load_library,
+    ssm_block_norm_bwd,
+    ssm_block_norm_bwd_workspace_bytes,
+    ssm_block_norm_fwd,
+    ssm_causal_conv1d_bwd,
+    ssm_causal_conv1d_bwd_workspace_bytes,
     ssm_causal_conv1d_fwd,
+    ssm_gated_scan_bwd,
+    ssm_gated_scan_bwd_workspace_bytes,
+    ssm_gated_scan_fwd,
+    ssm_gated_scan_fwd_train,
+    ssm_gated_scan_states_bytes,
+    ssm_gated_scan_workspace_bytes,
+    ssm_gated_state_update,
     ssm_scan_bwd,
     ssm_scan_bwd_ex,
     ssm_scan_bwd_ex_workspace_bytes,

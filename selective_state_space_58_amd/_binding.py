@@ -21,6 +21,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
 
 
 class SSMError(RuntimeError):
@@ -97,6 +98,28 @@ def load_library():
         lib.ssm_scan_bwd_workspace_bytes.restype = _SZ
         lib.ssm_scan_bwd_ex_workspace_bytes.argtypes = [_I64] * 4 + [_I]
         lib.ssm_scan_bwd_ex_workspace_bytes.restype = _SZ
+        lib.ssm_causal_conv1d_bwd.argtypes = [_P] * 4 + [_I] + [_P] * 6 + [_I64] * 4 + [_I, _P, _SZ, _P]
+        lib.ssm_causal_conv1d_bwd.restype = _I
+        lib.ssm_causal_conv1d_bwd_workspace_bytes.argtypes = [_I64] * 4
+        lib.ssm_causal_conv1d_bwd_workspace_bytes.restype = _SZ
+        lib.ssm_gated_scan_fwd.argtypes = [_P] * 9 + [_I64] * 3 + [_I, _I, _P, _SZ, _P]
+        lib.ssm_gated_scan_fwd.restype = _I
+        lib.ssm_gated_scan_workspace_bytes.argtypes = [_I64] * 3 + [_I]
+        lib.ssm_gated_scan_workspace_bytes.restype = _SZ
+        lib.ssm_gated_scan_states_bytes.argtypes = [_I64] * 3
+        lib.ssm_gated_scan_states_bytes.restype = _SZ
+        lib.ssm_gated_scan_bwd.argtypes = [_P] * 14 + [_I64] * 3 + [_I, _I, _P, _SZ, _P]
+        lib.ssm_gated_scan_bwd.restype = _I
+        lib.ssm_gated_scan_bwd_workspace_bytes.argtypes = [_I64] * 3 + [_I, _I]
+        lib.ssm_gated_scan_bwd_workspace_bytes.restype = _SZ
+        lib.ssm_gated_state_update.argtypes = [_P] * 6 + [_I64] * 2 + [_I, _I, _P]
+        lib.ssm_gated_state_update.restype = _I
+        lib.ssm_block_norm_fwd.argtypes = [_P] * 7 + [_F, _F, _P, _P] + [_I64] * 2 + [_I, _I, _P]
+        lib.ssm_block_norm_fwd.restype = _I
+        lib.ssm_block_norm_bwd.argtypes = [_P] * 7 + [_F, _F] + [_P] * 8 + [_I64] * 2 + [_I, _I, _P, _SZ, _P]
+        lib.ssm_block_norm_bwd.restype = _I
+        lib.ssm_block_norm_bwd_workspace_bytes.argtypes = [_I64] * 2
+        lib.ssm_block_norm_bwd_workspace_bytes.restype = _SZ
         lib.ssm_status_string.argtypes = [_I]
         lib.ssm_status_string.restype = ctypes.c_char_p
         lib.ssm_last_error.argtypes = []
@@ -501,4 +524,270 @@ def ssm_scan_bwd(x, delta, A, B, C, dout, D=None, z=None, delta_bias=None, delta
     else:
         rc = lib.ssm_scan_bwd_ex(*args, flags, _ptr(workspace), wsb, _stream(dev))
         _check(lib, "ssm_scan_bwd_ex", rc)
+    return g
+
+
+# forms of the gated scan (enum ssm_gated_form)
+SSM_GATED_LRU = 0
+SSM_GATED_UNIT = 1
+
+
+def _on(dev):
+    """The library's kernels run on the current device: make it the tensors'."""
+    return torch.cuda.device(dev)
+
+
+def _workspace(workspace, nbytes, dev):
+    """The caller's workspace, checked, or one of torch's (from its stream-ordered pool, so that a call
+    under graph capture takes the graph's own)."""
+    if workspace is None:
+        return (torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes) if nbytes > 0 else (None, 0)
+    _need(workspace, "workspace", device=dev)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def ssm_causal_conv1d_bwd_workspace_bytes(batch, seqlen, dim, width) -> int:
+    return int(load_library().ssm_causal_conv1d_bwd_workspace_bytes(batch, seqlen, dim, width))
+
+
+def ssm_causal_conv1d_bwd(x, weight, dout, bias=None, state_in=None, silu=True, dstate_out=None,
+                          want_dstate_in=False, workspace=None):
+    """Gradients of sum(dout * out) + sum(dstate_out * state_out) for ssm_causal_conv1d_fwd with the same
+    inputs.  Returns a dict: dx (x's dtype), dweight (fp32) and, with bias, dbias (fp32), with state_in or
+    want_dstate_in, dstate_in (x's dtype)."""
+    lib = load_library()
+    _need(x, "x")
+    dev = x.device
+    if x.dim() != 3:
+        raise ValueError("x must be (batch, seqlen, dim)")
+    batch, seqlen, dim = x.shape
+    act = _act_code(x, "x")
+    _need(weight, "weight", torch.float32, device=dev)
+    if weight.dim() != 2 or weight.shape[0] != dim:
+        raise ValueError("weight must be (dim, width)")
+    width = weight.shape[1]
+    _need(dout, "dout", x.dtype, x.shape, dev)
+    _need(bias, "bias", torch.float32, (dim,), dev)
+    _need(state_in, "state_in", x.dtype, (batch, dim, width - 1), dev)
+    _need(dstate_out, "dstate_out", x.dtype, (batch, dim, width - 1), dev)
+    with _on(dev):
+        g = dict(dx=torch.empty_like(x), dweight=torch.empty_like(weight))
+        if bias is not None:
+            g["dbias"] = torch.empty_like(bias)
+        if state_in is not None or want_dstate_in:
+            g["dstate_in"] = torch.empty((batch, dim, width - 1), dtype=x.dtype, device=dev)
+        ws, wsb = _workspace(workspace, ssm_causal_conv1d_bwd_workspace_bytes(batch, seqlen, dim, width), dev)
+        rc = lib.ssm_causal_conv1d_bwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(state_in), int(bool(silu)), _ptr(dout),
+                                       _ptr(dstate_out), _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(g.get("dbias")),
+                                       _ptr(g.get("dstate_in")), batch, seqlen, dim, width, act, _ptr(ws), wsb,
+                                       _stream(dev))
+    _check(lib, "ssm_causal_conv1d_bwd", rc)
+    return g
+
+
+def ssm_gated_scan_workspace_bytes(batch, seqlen, dim, dtype=torch.bfloat16) -> int:
+    return int(load_library().ssm_gated_scan_workspace_bytes(batch, seqlen, dim, _DT[dtype]))
+
+
+def ssm_gated_scan_states_bytes(batch, seqlen, dim) -> int:
+    return int(load_library().ssm_gated_scan_states_bytes(batch, seqlen, dim))
+
+
+def ssm_gated_scan_bwd_workspace_bytes(batch, seqlen, dim, dtype=torch.bfloat16, have_states=True) -> int:
+    return int(load_library().ssm_gated_scan_bwd_workspace_bytes(batch, seqlen, dim, _DT[dtype], int(have_states)))
+
+
+def _gated_inputs(x, r, i, A, ndim):
+    """Checks shared by the gated calls; returns (form, act code, device)."""
+    _need(x, "x")
+    dev = x.device
+    if x.dim() != ndim:
+        raise ValueError("x must be (batch, seqlen, dim)" if ndim == 3 else "x must be (batch, dim)")
+    act = _act_code(x, "x")
+    _need(r, "r", x.dtype, x.shape, dev)
+    if (i is None) != (A is None):
+        raise ValueError("i and A go together: both (a = exp(A sigmoid(r))) or neither (a = sigmoid(r))")
+    _need(i, "i", x.dtype, x.shape, dev)
+    _need(A, "A", torch.float32, (x.shape[-1],), dev)
+    return (SSM_GATED_UNIT if A is None else SSM_GATED_LRU), act, dev
+
+
+def _reset(reset, shape, dev):
+    if reset is not None and isinstance(reset, torch.Tensor) and reset.dtype not in (torch.bool, torch.uint8):
+        raise TypeError("reset must be bool or uint8, got %s" % reset.dtype)
+    return _need(reset, "reset", shape=shape, device=dev)
+
+
+def ssm_gated_scan_fwd(x, r, i=None, A=None, reset=None, h0=None, return_final_state=False, y=None, h_final=None,
+                       workspace=None):
+    """Gated linear recurrence over a sequence, h = a h + b, y = h.  x, r, i: (batch, seqlen, dim);
+    A: (dim) fp32; reset: (batch, seqlen) bool or uint8, a = 0 where set; h0: (batch, dim) fp32.
+    With i and A: a = exp(A sigmoid(r)), b = sqrt(1 - a^2) sigmoid(i) x.  Without: a = sigmoid(r),
+    b = (1 - a) x.  Returns y, or (y, h_final) with return_final_state."""
+    return _gated_fwd("ssm_gated_scan_fwd", x, r, i, A, reset, h0, return_final_state, y, h_final, None, workspace)
+
+
+def ssm_gated_scan_fwd_train(x, r, i=None, A=None, reset=None, h0=None, return_final_state=False, y=None,
+                             h_final=None, states=None, workspace=None):
+    """ssm_gated_scan_fwd that also returns the states entering every 64th token, fp32
+    (ceil(seqlen/64), batch, dim), for ssm_gated_scan_bwd.  Returns (y, states) or (y, h_final, states)."""
+    _need(x, "x")
+    if x.dim() != 3:
+        raise ValueError("x must be (batch, seqlen, dim)")
+    shape = ((x.shape[1] + 63) // 64, x.shape[0], x.shape[2])
+    if states is None:
+        states = torch.empty(shape, dtype=torch.float32, device=x.device)
+    _need(states, "states", torch.float32, shape, x.device)
+    out = _gated_fwd("ssm_gated_scan_fwd_train", x, r, i, A, reset, h0, return_final_state, y, h_final, states,
+                     workspace)
+    return (*out, states) if isinstance(out, tuple) else (out, states)
+
+
+def _gated_fwd(name, x, r, i, A, reset, h0, return_final_state, y, h_final, states, workspace):
+    lib = load_library()
+    form, act, dev = _gated_inputs(x, r, i, A, 3)
+    batch, seqlen, dim = x.shape
+    _reset(reset, (batch, seqlen), dev)
+    _need(h0, "h0", torch.float32, (batch, dim), dev)
+    with _on(dev):
+        if y is None:
+            y = torch.empty_like(x)
+        _need(y, "y", x.dtype, x.shape, dev)
+        if return_final_state and h_final is None:
+            h_final = torch.empty((batch, dim), dtype=torch.float32, device=dev)
+        _need(h_final, "h_final", torch.float32, (batch, dim), dev)
+        ws, wsb = _workspace(workspace, lib.ssm_gated_scan_workspace_bytes(batch, seqlen, dim, act), dev)
+        rc = lib.ssm_gated_scan_fwd(_ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(reset), _ptr(h0), _ptr(y), _ptr(h_final),
+                                    _ptr(states), batch, seqlen, dim, form, act, _ptr(ws), wsb, _stream(dev))
+    _check(lib, name, rc)
+    return (y, h_final) if (return_final_state or h_final is not None) else y
+
+
+def ssm_gated_scan_bwd(x, r, dout, i=None, A=None, reset=None, h0=None, dh_final=None, states=None, want_dh0=False,
+                       workspace=None):
+    """Gradients of sum(dout * y) + sum(dh_final * h_final) for ssm_gated_scan_fwd with the same inputs.
+    states: what ssm_gated_scan_fwd_train returned for them (without, they are computed first).  Returns a
+    dict: dx, dr (x's dtype), with i and A also di (x's dtype) and dA (fp32), with h0 or want_dh0 dh0."""
+    lib = load_library()
+    form, act, dev = _gated_inputs(x, r, i, A, 3)
+    batch, seqlen, dim = x.shape
+    _reset(reset, (batch, seqlen), dev)
+    _need(dout, "dout", x.dtype, x.shape, dev)
+    _need(h0, "h0", torch.float32, (batch, dim), dev)
+    _need(dh_final, "dh_final", torch.float32, (batch, dim), dev)
+    _need(states, "states", torch.float32, ((seqlen + 63) // 64, batch, dim), dev)
+    with _on(dev):
+        g = dict(dx=torch.empty_like(x), dr=torch.empty_like(x))
+        if form == SSM_GATED_LRU:
+            g["di"] = torch.empty_like(x)
+            g["dA"] = torch.empty_like(A)
+        if h0 is not None or want_dh0:
+            g["dh0"] = torch.empty((batch, dim), dtype=torch.float32, device=dev)
+        have = int(states is not None and states.numel() > 0)
+        ws, wsb = _workspace(workspace, lib.ssm_gated_scan_bwd_workspace_bytes(batch, seqlen, dim, act, have), dev)
+        rc = lib.ssm_gated_scan_bwd(_ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(reset), _ptr(h0),
+                                    _ptr(states) if have else None, _ptr(dout), _ptr(dh_final), _ptr(g["dx"]),
+                                    _ptr(g["dr"]), _ptr(g.get("di")), _ptr(g.get("dA")), _ptr(g.get("dh0")),
+                                    batch, seqlen, dim, form, act, _ptr(ws), wsb, _stream(dev))
+    _check(lib, "ssm_gated_scan_bwd", rc)
+    return g
+
+
+def ssm_gated_state_update(x, r, state, i=None, A=None, y=None):
+    """One token of ssm_gated_scan_fwd.  x, r, i: (batch, dim); A: (dim) fp32; state: (batch, dim) fp32,
+    updated in place.  Returns y (batch, dim)."""
+    lib = load_library()
+    form, act, dev = _gated_inputs(x, r, i, A, 2)
+    batch, dim = x.shape
+    _need(state, "state", torch.float32, (batch, dim), dev)
+    with _on(dev):
+        if y is None:
+            y = torch.empty_like(x)
+        _need(y, "y", x.dtype, x.shape, dev)
+        rc = lib.ssm_gated_state_update(_ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(state), _ptr(y), batch, dim, form,
+                                        act, _stream(dev))
+    _check(lib, "ssm_gated_state_update", rc)
+    return y
+
+
+def _norm_inputs(y, z, residual, w_post, scale, w_pre, p, rng, res_dtype):
+    """Checks shared by the block norm's directions; returns (rows, dim, act code, res dtype, device)."""
+    _need(y, "y")
+    dev = y.device
+    if y.dim() < 1:
+        raise ValueError("y must be (..., dim)")
+    dim = y.shape[-1]
+    rows = y.numel() // dim if dim > 0 else 0
+    act = _act_code(y, "y")
+    _need(z, "z", y.dtype, y.shape, dev)
+    if residual is not None:
+        _need(residual, "residual", shape=y.shape, device=dev)
+        if res_dtype is not None and res_dtype != residual.dtype:
+            raise TypeError("res_dtype must be residual's dtype")
+        res_dtype = residual.dtype
+    res_dtype = y.dtype if res_dtype is None else res_dtype
+    if res_dtype not in _DT:
+        raise TypeError("residual and res_dtype must be float32 or bfloat16")
+    for t, name in ((w_post, "w_post"), (scale, "scale"), (w_pre, "w_pre")):
+        _need(t, name, torch.float32, (dim,), dev)
+    if p > 0 and rng is None:
+        raise ValueError("rng is required when p > 0")
+    _need(rng, "rng", torch.int64, (2,), dev)
+    return rows, dim, act, res_dtype, dev
+
+
+def ssm_block_norm_fwd(y, z=None, residual=None, w_post=None, scale=None, w_pre=None, p=0.0, rng=None, eps=1e-5,
+                       res_dtype=None, res_out=None, out=None):
+    """Gate, norm after a block, residual scale, dropout, residual sum and norm before the next block:
+    R = residual + dropout_p(scale * rmsnorm(y * silu(z)) * w_post), out = rmsnorm(R) * w_pre, each part
+    left out where its argument is None.  y, z: (..., dim); residual: the same shape, fp32 or bf16;
+    w_post, scale, w_pre: (dim) fp32; rng: (2) int64 on the device (seed, offset), read when p > 0;
+    res_dtype: R's dtype without a residual (y's by default).  Returns R, or (R, out) with w_pre."""
+    lib = load_library()
+    rows, dim, act, res_dtype, dev = _norm_inputs(y, z, residual, w_post, scale, w_pre, p, rng, res_dtype)
+    with _on(dev):
+        if res_out is None:
+            res_out = torch.empty(y.shape, dtype=res_dtype, device=dev)
+        _need(res_out, "res_out", res_dtype, y.shape, dev)
+        if out is None and w_pre is not None:
+            out = torch.empty_like(y)
+        _need(out, "out", y.dtype, y.shape, dev)
+        rc = lib.ssm_block_norm_fwd(_ptr(y), _ptr(z), _ptr(residual), _ptr(w_post), _ptr(scale), _ptr(w_pre), _ptr(rng),
+                                    p, eps, _ptr(res_out), _ptr(out), rows, dim, act, _DT[res_dtype], _stream(dev))
+    _check(lib, "ssm_block_norm_fwd", rc)
+    return res_out if w_pre is None else (res_out, out)
+
+
+def ssm_block_norm_bwd_workspace_bytes(rows, dim) -> int:
+    return int(load_library().ssm_block_norm_bwd_workspace_bytes(rows, dim))
+
+
+def ssm_block_norm_bwd(y, dres=None, dout=None, z=None, residual=None, w_post=None, scale=None, w_pre=None, p=0.0,
+                       rng=None, eps=1e-5, res_dtype=None, workspace=None):
+    """Gradients of sum(dres * R) + sum(dout * out) for ssm_block_norm_fwd with the same inputs (rng holding
+    the same numbers).  Returns a dict: dy and, for the optional inputs given, dz, dresidual, dw_post,
+    dscale, dw_pre (the last three fp32)."""
+    lib = load_library()
+    if residual is None and res_dtype is None and isinstance(dres, torch.Tensor):
+        res_dtype = dres.dtype
+    rows, dim, act, res_dtype, dev = _norm_inputs(y, z, residual, w_post, scale, w_pre, p, rng, res_dtype)
+    _need(dres, "dres", res_dtype, y.shape, dev)
+    _need(dout, "dout", y.dtype, y.shape, dev)
+    if (dout is None) != (w_pre is None) or (dres is None and dout is None):
+        raise ValueError("dout goes with w_pre, and dout or dres is required")
+    with _on(dev):
+        g = dict(dy=torch.empty_like(y))
+        if z is not None:
+            g["dz"] = torch.empty_like(y)
+        if residual is not None:
+            g["dresidual"] = torch.empty_like(residual)
+        for t, name in ((w_post, "dw_post"), (scale, "dscale"), (w_pre, "dw_pre")):
+            if t is not None:
+                g[name] = torch.empty_like(t)
+        ws, wsb = _workspace(workspace, ssm_block_norm_bwd_workspace_bytes(rows, dim), dev)
+        rc = lib.ssm_block_norm_bwd(_ptr(y), _ptr(z), _ptr(residual), _ptr(w_post), _ptr(scale), _ptr(w_pre), _ptr(rng),
+                                    p, eps, _ptr(dres), _ptr(dout), _ptr(g["dy"]), _ptr(g.get("dz")),
+                                    _ptr(g.get("dresidual")), _ptr(g.get("dw_post")), _ptr(g.get("dscale")),
+                                    _ptr(g.get("dw_pre")), rows, dim, act, _DT[res_dtype], _ptr(ws), wsb, _stream(dev))
+    _check(lib, "ssm_block_norm_bwd", rc)
     return g

@@ -35,6 +35,12 @@ bool aligned16(const void* p) { return aligned(p, 16); }
 
 size_t dsize(int dt) { return dt == SSM_BF16 ? 2 : 4; }
 
+// Whether two buffers share a byte (a null or empty one shares none).
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const char *p = (const char*)a, *q = (const char*)b;
+  return p != nullptr && q != nullptr && na > 0 && nb > 0 && p < q + nb && q < p + na;
+}
+
 // Stream-ordered scratch for calls that pass no workspace.
 struct Scratch {
   void* ptr = nullptr;
@@ -520,6 +526,270 @@ int ssm_scan_bwd_train(const void* x, const void* delta, const float* A, const v
   return bwd_common(x, delta, A, B, C, Dskip, z, delta_bias, delta_softplus, h0, dout, dh_final, dx, ddelta, dA, dB,
                     dC, dDskip, dz, ddelta_bias, dh0, batch, seqlen, dim, dstate, act_dtype, delta_dtype, flags,
                     workspace, workspace_bytes, stream, states, true);
+}
+
+size_t ssm_causal_conv1d_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t width) {
+  if (batch <= 0 || seqlen <= 0 || dim <= 0 || width <= 0 || width > 8) return 0;
+  if (!elems_ok({batch, seqlen, dim}) || !elems_ok({dim, width})) return 0;
+  return conv_bwd_ws_bytes(batch, seqlen, dim, width, device_cu_count());
+}
+
+int ssm_causal_conv1d_bwd(const void* x, const float* weight, const float* bias, const void* state_in, int silu,
+                          const void* dout, const void* dstate_out, void* dx, float* dweight, float* dbias,
+                          void* dstate_in, int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int act_dtype,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (batch < 0 || seqlen < 0 || dim < 0 || width < 0) return fail(SSM_ERR_SHAPE, "negative size");
+  if (width == 0) return fail(SSM_ERR_SHAPE, "width must be >= 1");
+  if (silu != 0 && silu != 1) return fail(SSM_ERR_SHAPE, "silu must be 0 or 1");
+  if (act_dtype != SSM_F32 && act_dtype != SSM_BF16) return fail(SSM_ERR_DTYPE, "act_dtype must be SSM_F32 or SSM_BF16");
+  const bool has_tok = batch > 0 && seqlen > 0 && dim > 0;
+  if ((has_tok && (x == nullptr || dout == nullptr || dx == nullptr)) ||
+      (dim > 0 && (weight == nullptr || dweight == nullptr || (bias != nullptr && dbias == nullptr))))
+    return fail(SSM_ERR_NULL, "x, weight, dout, dx, dweight and, with bias, dbias are required");
+  if (!elems_ok({batch, seqlen, dim}) || !elems_ok({dim, width}) || !elems_ok({batch, dim, width}))
+    return fail(SSM_ERR_SHAPE, "sizes overflow 64-bit indexing");
+  if (width > 8) return fail(SSM_ERR_UNSUPPORTED, "conv width > 8 is not supported");
+  const size_t as = dsize(act_dtype);
+  if (!aligned(x, as) || !aligned(dout, as) || !aligned(dx, as) || !aligned(state_in, as) || !aligned(dstate_out, as) ||
+      !aligned(dstate_in, as) || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(dweight, 4) || !aligned(dbias, 4))
+    return fail(SSM_ERR_ALIGNMENT, "a pointer is not aligned to its element size");
+  if (dim == 0) return SSM_OK;
+  const size_t n = (size_t)(batch * seqlen * dim) * as, ns = (size_t)(batch * dim * (width - 1)) * as;
+  if (overlap(dx, n, x, n) || overlap(dx, n, dout, n) || overlap(dstate_in, ns, dstate_out, ns) ||
+      overlap(dstate_in, ns, state_in, ns))
+    return fail(SSM_ERR_SHAPE, "outputs must not overlap inputs");
+  Scratch own;
+  void* ws = nullptr;
+  int rc = get_workspace(workspace, workspace_bytes, ssm_causal_conv1d_bwd_workspace_bytes(batch, seqlen, dim, width),
+                         (hipStream_t)stream, &own, &ws);
+  if (rc != SSM_OK) return rc;
+  ConvBwdArgs a{};
+  a.x = x; a.w = weight; a.bias = bias; a.state_in = state_in; a.dout = dout; a.dstate_out = dstate_out;
+  a.dx = dx; a.dweight = dweight; a.dbias = bias != nullptr ? dbias : nullptr; a.dstate_in = dstate_in;
+  a.ws = (float*)ws;
+  a.batch = batch; a.seqlen = seqlen; a.dim = dim; a.width = width; a.silu = silu;
+  a.act_bf16 = act_dtype == SSM_BF16;
+  a.vec = dim % 4 == 0 && aligned(x, 4 * as) && aligned(dout, 4 * as) && aligned(dx, 4 * as);
+  return launch_conv_bwd(a, device_cu_count(), stream);
+}
+
+static int validate_gated(const void* x, const void* r, const void* i, const float* A, bool has_tok, int64_t batch,
+                          int64_t seqlen, int64_t dim, int form, int act_dtype) {
+  if (batch < 0 || seqlen < 0 || dim < 0) return fail(SSM_ERR_SHAPE, "negative size");
+  if (form != SSM_GATED_LRU && form != SSM_GATED_UNIT) return fail(SSM_ERR_UNSUPPORTED, "unknown gated form");
+  if (act_dtype != SSM_F32 && act_dtype != SSM_BF16) return fail(SSM_ERR_DTYPE, "act_dtype must be SSM_F32 or SSM_BF16");
+  if (has_tok && (x == nullptr || r == nullptr)) return fail(SSM_ERR_NULL, "x and r are required");
+  if (form == SSM_GATED_LRU && ((has_tok && i == nullptr) || (dim > 0 && A == nullptr)))
+    return fail(SSM_ERR_NULL, "SSM_GATED_LRU needs i and A");
+  if (form == SSM_GATED_UNIT && (i != nullptr || A != nullptr))
+    return fail(SSM_ERR_SHAPE, "SSM_GATED_UNIT takes neither i nor A");
+  if (!elems_ok({batch, seqlen, dim}) || !elems_ok({batch, dim}))
+    return fail(SSM_ERR_SHAPE, "sizes overflow 64-bit indexing");
+  return SSM_OK;
+}
+
+size_t ssm_gated_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int act_dtype) {
+  if (batch <= 0 || seqlen <= 0 || dim <= 0 || !elems_ok({batch, seqlen, dim})) return 0;
+  return plan_gated(batch, seqlen, dim, act_dtype == SSM_BF16, device_cu_count()).maps_bytes;
+}
+
+size_t ssm_gated_scan_states_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
+  if (batch <= 0 || seqlen <= 0 || dim <= 0 || !elems_ok({batch, seqlen, dim})) return 0;
+  return plan_gated(batch, seqlen, dim, true, device_cu_count()).states_bytes;
+}
+
+size_t ssm_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int act_dtype, int have_states) {
+  if (batch <= 0 || seqlen < 0 || dim <= 0 || !elems_ok({batch, seqlen, dim})) return 0;
+  const GatedPlan p = plan_gated(batch, seqlen, dim, act_dtype == SSM_BF16, device_cu_count());
+  return p.maps_bytes + p.da_bytes + (have_states ? 0 : p.states_bytes);
+}
+
+int ssm_gated_scan_fwd(const void* x, const void* r, const void* i, const float* A, const uint8_t* reset,
+                       const float* h0, void* y, float* h_final, float* states, int64_t batch, int64_t seqlen,
+                       int64_t dim, int form, int act_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  const bool has_tok = batch > 0 && seqlen > 0 && dim > 0;
+  int rc = validate_gated(x, r, i, A, has_tok, batch, seqlen, dim, form, act_dtype);
+  if (rc != SSM_OK) return rc;
+  if (has_tok && y == nullptr) return fail(SSM_ERR_NULL, "y is required");
+  const size_t as = dsize(act_dtype);
+  if (!aligned(x, as) || !aligned(r, as) || !aligned(i, as) || !aligned(y, as) || !aligned(A, 4) || !aligned(h0, 4) ||
+      !aligned(h_final, 4) || !aligned(states, 4))
+    return fail(SSM_ERR_ALIGNMENT, "a pointer is not aligned to its element size");
+  if (batch == 0 || dim == 0) return SSM_OK;
+  const size_t n = (size_t)(batch * seqlen * dim) * as;
+  if (overlap(y, n, x, n) || overlap(y, n, r, n) || overlap(y, n, i, n))
+    return fail(SSM_ERR_SHAPE, "y must not overlap an input");
+  const GatedPlan p = plan_gated(batch, seqlen, dim, act_dtype == SSM_BF16, device_cu_count());
+  Scratch own;
+  void* ws = nullptr;
+  rc = get_workspace(workspace, workspace_bytes, p.maps_bytes, (hipStream_t)stream, &own, &ws);
+  if (rc != SSM_OK) return rc;
+  GatedArgs a{};
+  a.x = x; a.r = r; a.i = i; a.A = A; a.reset = reset; a.h0 = h0; a.y = y; a.h_final = h_final; a.states = states;
+  a.batch = batch; a.seqlen = seqlen; a.dim = dim; a.form = form; a.act_bf16 = act_dtype == SSM_BF16;
+  a.vec = dim % 2 == 0 && aligned(x, 2 * as) && aligned(r, 2 * as) && aligned(i, 2 * as) && aligned(y, 2 * as);
+  return launch_gated_fwd(a, p, ws, stream);
+}
+
+int ssm_gated_scan_bwd(const void* x, const void* r, const void* i, const float* A, const uint8_t* reset,
+                       const float* h0, const float* states, const void* dout, const float* dh_final, void* dx,
+                       void* dr, void* di, float* dA, float* dh0, int64_t batch, int64_t seqlen, int64_t dim, int form,
+                       int act_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  const bool has_tok = batch > 0 && seqlen > 0 && dim > 0;
+  int rc = validate_gated(x, r, i, A, has_tok, batch, seqlen, dim, form, act_dtype);
+  if (rc != SSM_OK) return rc;
+  if ((has_tok && (dout == nullptr || dx == nullptr || dr == nullptr)) ||
+      (form == SSM_GATED_LRU && ((has_tok && di == nullptr) || (dim > 0 && dA == nullptr))))
+    return fail(SSM_ERR_NULL, "dout, dx, dr and, for SSM_GATED_LRU, di and dA are required");
+  const size_t as = dsize(act_dtype);
+  if (!aligned(x, as) || !aligned(r, as) || !aligned(i, as) || !aligned(dout, as) || !aligned(dx, as) ||
+      !aligned(dr, as) || !aligned(di, as) || !aligned(A, 4) || !aligned(h0, 4) || !aligned(states, 4) ||
+      !aligned(dh_final, 4) || !aligned(dA, 4) || !aligned(dh0, 4))
+    return fail(SSM_ERR_ALIGNMENT, "a pointer is not aligned to its element size");
+  if (dim == 0) return SSM_OK;
+  const size_t n = (size_t)(batch * seqlen * dim) * as;
+  const void* in[] = {x, r, i, dout};
+  const void* out[] = {dx, dr, form == SSM_GATED_LRU ? di : nullptr};
+  for (const void* o : out)
+    for (const void* q : in)
+      if (overlap(o, n, q, n)) return fail(SSM_ERR_SHAPE, "outputs must not overlap inputs");
+  const GatedPlan p = plan_gated(batch, seqlen, dim, act_dtype == SSM_BF16, device_cu_count());
+  Scratch own;
+  void* ws = nullptr;
+  rc = get_workspace(workspace, workspace_bytes, p.maps_bytes + p.da_bytes + (states != nullptr ? 0 : p.states_bytes),
+                     (hipStream_t)stream, &own, &ws);
+  if (rc != SSM_OK) return rc;
+  GatedArgs a{};
+  a.x = x; a.r = r; a.i = i; a.A = A; a.reset = reset; a.h0 = h0; a.saved = states; a.dout = dout;
+  a.dh_final = dh_final; a.dx = dx; a.dr = dr; a.di = di; a.dA = dA; a.dh0 = dh0;
+  a.batch = batch; a.seqlen = seqlen; a.dim = dim; a.form = form; a.act_bf16 = act_dtype == SSM_BF16;
+  a.vec = dim % 2 == 0;
+  for (const void* q : in) a.vec = a.vec && aligned(q, 2 * as);
+  for (const void* o : out) a.vec = a.vec && aligned(o, 2 * as);
+  return launch_gated_bwd(a, p, ws, stream);
+}
+
+int ssm_gated_state_update(const void* x, const void* r, const void* i, const float* A, float* state, void* y,
+                           int64_t batch, int64_t dim, int form, int act_dtype, void* stream) {
+  g_last_error.clear();
+  const bool has = batch > 0 && dim > 0;
+  int rc = validate_gated(x, r, i, A, has, batch, 1, dim, form, act_dtype);
+  if (rc != SSM_OK) return rc;
+  if (has && (state == nullptr || y == nullptr)) return fail(SSM_ERR_NULL, "state and y are required");
+  const size_t as = dsize(act_dtype);
+  if (!aligned(x, as) || !aligned(r, as) || !aligned(i, as) || !aligned(y, as) || !aligned(A, 4) || !aligned(state, 4))
+    return fail(SSM_ERR_ALIGNMENT, "a pointer is not aligned to its element size");
+  if (!has) return SSM_OK;
+  const size_t n = (size_t)(batch * dim) * as, ns = (size_t)(batch * dim) * 4;
+  if (overlap(y, n, state, ns) || overlap(y, n, x, n) || overlap(y, n, r, n) || overlap(y, n, i, n))
+    return fail(SSM_ERR_SHAPE, "y must not overlap the state or an input");
+  GatedArgs a{};
+  a.x = x; a.r = r; a.i = i; a.A = A; a.states = state; a.y = y;
+  a.batch = batch; a.dim = dim; a.seqlen = 1; a.form = form; a.act_bf16 = act_dtype == SSM_BF16;
+  a.vec = dim % 2 == 0 && aligned(x, 2 * as) && aligned(r, 2 * as) && aligned(i, 2 * as) && aligned(y, 2 * as);
+  return launch_gated_step(a, stream);
+}
+
+// Checks shared by the block norm's two directions; fills what they share.
+static int norm_common(NormArgs& a, const void* y, const void* z, const void* residual, const float* w_post,
+                       const float* scale, const float* w_pre, const int64_t* rng, float p, float eps, int64_t rows,
+                       int64_t dim, int act_dtype, int res_dtype) {
+  if (rows < 0 || dim < 0) return fail(SSM_ERR_SHAPE, "negative size");
+  if (!elems_ok({rows, dim})) return fail(SSM_ERR_SHAPE, "sizes overflow 64-bit indexing");
+  if (dim > kNormMaxDim) return fail(SSM_ERR_UNSUPPORTED, "dim > 16384 is not supported");
+  if ((act_dtype != SSM_F32 && act_dtype != SSM_BF16) || (res_dtype != SSM_F32 && res_dtype != SSM_BF16))
+    return fail(SSM_ERR_DTYPE, "act_dtype and res_dtype must be SSM_F32 or SSM_BF16");
+  if (!(p >= 0.f && p < 1.f)) return fail(SSM_ERR_SHAPE, "p must be in [0, 1)");
+  if (!(eps > 0.f) || eps > std::numeric_limits<float>::max()) return fail(SSM_ERR_SHAPE, "eps must be positive");
+  const unsigned drop = (unsigned)(p * 65536.f + 0.5f);
+  if (drop > 65535u) return fail(SSM_ERR_UNSUPPORTED, "p is within 2^-17 of 1");
+  if ((rows > 0 && dim > 0 && y == nullptr) || (drop > 0 && rng == nullptr))
+    return fail(SSM_ERR_NULL, "y and, with p > 0, rng are required");
+  const size_t as = dsize(act_dtype), rs = dsize(res_dtype);
+  if (!aligned(y, as) || !aligned(z, as) || !aligned(residual, rs) || !aligned(w_post, 4) || !aligned(scale, 4) ||
+      !aligned(w_pre, 4) || !aligned(rng, 8))
+    return fail(SSM_ERR_ALIGNMENT, "a pointer is not aligned to its element size");
+  a.y = y; a.z = z; a.residual = residual; a.w_post = w_post; a.scale = scale; a.w_pre = w_pre; a.rng = rng;
+  a.rows = rows; a.dim = dim; a.eps = eps; a.drop = drop; a.keep_scale = 65536.f / (65536.f - (float)drop);
+  a.act_bf16 = act_dtype == SSM_BF16; a.res_bf16 = res_dtype == SSM_BF16;
+  a.vec = dim % 8 == 0 && aligned16(y) && aligned16(z) && aligned16(residual) && aligned16(w_post) &&
+          aligned16(scale) && aligned16(w_pre);
+  return SSM_OK;
+}
+
+int ssm_block_norm_fwd(const void* y, const void* z, const void* residual, const float* w_post, const float* scale,
+                       const float* w_pre, const int64_t* rng, float p, float eps, void* res_out, void* out,
+                       int64_t rows, int64_t dim, int act_dtype, int res_dtype, void* stream) {
+  g_last_error.clear();
+  NormArgs a{};
+  int rc = norm_common(a, y, z, residual, w_post, scale, w_pre, rng, p, eps, rows, dim, act_dtype, res_dtype);
+  if (rc != SSM_OK) return rc;
+  if ((out != nullptr) != (w_pre != nullptr) && rows > 0 && dim > 0)
+    return fail(SSM_ERR_NULL, "out and w_pre go together");
+  if (rows > 0 && dim > 0 && out == nullptr && res_out == nullptr)
+    return fail(SSM_ERR_NULL, "res_out or out is required");
+  const size_t as = dsize(act_dtype), rs = dsize(res_dtype);
+  if (!aligned(res_out, rs) || !aligned(out, as))
+    return fail(SSM_ERR_ALIGNMENT, "a pointer is not aligned to its element size");
+  if (rows == 0 || dim == 0) return SSM_OK;
+  const size_t n = (size_t)(rows * dim);
+  if (overlap(res_out, n * rs, y, n * as) || overlap(res_out, n * rs, z, n * as) || overlap(out, n * as, y, n * as) ||
+      overlap(out, n * as, z, n * as) || overlap(out, n * as, residual, n * rs) || overlap(out, n * as, res_out, n * rs) ||
+      (res_out != residual && overlap(res_out, n * rs, residual, n * rs)))
+    return fail(SSM_ERR_SHAPE, "outputs must not overlap inputs (res_out may be residual)");
+  a.res_out = res_out; a.out = out;
+  a.vec = a.vec && aligned16(res_out) && aligned16(out);
+  return launch_norm_fwd(a, stream);
+}
+
+size_t ssm_block_norm_bwd_workspace_bytes(int64_t rows, int64_t dim) {
+  if (rows <= 0 || dim <= 0 || dim > kNormMaxDim || !elems_ok({rows, dim})) return 0;
+  return norm_bwd_ws_bytes(rows, dim);
+}
+
+int ssm_block_norm_bwd(const void* y, const void* z, const void* residual, const float* w_post, const float* scale,
+                       const float* w_pre, const int64_t* rng, float p, float eps, const void* dres, const void* dout,
+                       void* dy, void* dz, void* dresidual, float* dw_post, float* dscale, float* dw_pre, int64_t rows,
+                       int64_t dim, int act_dtype, int res_dtype, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  g_last_error.clear();
+  NormArgs a{};
+  int rc = norm_common(a, y, z, residual, w_post, scale, w_pre, rng, p, eps, rows, dim, act_dtype, res_dtype);
+  if (rc != SSM_OK) return rc;
+  const bool has = rows > 0 && dim > 0;
+  if (has && ((dout != nullptr) != (w_pre != nullptr) || (dout == nullptr && dres == nullptr)))
+    return fail(SSM_ERR_NULL, "dout goes with w_pre, and dout or dres is required");
+  if ((has && (dy == nullptr || (z != nullptr && dz == nullptr) || (residual != nullptr && dresidual == nullptr))) ||
+      (dim > 0 && ((w_post != nullptr && dw_post == nullptr) || (scale != nullptr && dscale == nullptr) ||
+                   (w_pre != nullptr && dw_pre == nullptr))))
+    return fail(SSM_ERR_NULL, "dy and the gradients of the optional inputs given are required");
+  const size_t as = dsize(act_dtype), rs = dsize(res_dtype);
+  if (!aligned(dres, rs) || !aligned(dout, as) || !aligned(dy, as) || !aligned(dz, as) || !aligned(dresidual, rs) ||
+      !aligned(dw_post, 4) || !aligned(dscale, 4) || !aligned(dw_pre, 4))
+    return fail(SSM_ERR_ALIGNMENT, "a pointer is not aligned to its element size");
+  if (dim == 0) return SSM_OK;
+  const size_t n = (size_t)(rows * dim);
+  const struct { const void* p; size_t b; } in[] = {{y, n * as}, {z, n * as}, {residual, n * rs}, {dres, n * rs}, {dout, n * as}},
+      out[] = {{dy, n * as}, {z != nullptr ? dz : nullptr, n * as}, {residual != nullptr ? dresidual : nullptr, n * rs}};
+  for (const auto& o : out)
+    for (const auto& q : in)
+      if (overlap(o.p, o.b, q.p, q.b)) return fail(SSM_ERR_SHAPE, "outputs must not overlap inputs");
+  Scratch own;
+  void* ws = nullptr;
+  rc = get_workspace(workspace, workspace_bytes, ssm_block_norm_bwd_workspace_bytes(rows, dim), (hipStream_t)stream, &own,
+                     &ws);
+  if (rc != SSM_OK) return rc;
+  a.dres = dres; a.dout = dout; a.dy = dy; a.ws = (float*)ws;
+  a.dz = z != nullptr ? dz : nullptr;
+  a.dresidual = residual != nullptr ? dresidual : nullptr;
+  a.dw_post = w_post != nullptr ? dw_post : nullptr;
+  a.dscale = scale != nullptr ? dscale : nullptr;
+  a.dw_pre = w_pre != nullptr ? dw_pre : nullptr;
+  a.vec = a.vec && aligned16(dres) && aligned16(dout) && aligned16(dy) && aligned16(a.dz) && aligned16(a.dresidual);
+  return launch_norm_bwd(a, stream);
 }
 
 }  // extern "C"

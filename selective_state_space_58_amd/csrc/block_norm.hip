@@ -1,0 +1,516 @@
+// What stands between two residual blocks, in one pass over the rows.  Per row,
+// in fp32 (every part in brackets is optional):
+//   v   = y [silu(z)]
+//   n   = [v / sqrt(mean v^2 + eps) w_post]
+//   m   = [scale] n
+//   R   = [residual +] [dropout] m
+//   out = [R / sqrt(mean R^2 + eps) w_pre]
+// and its gradient, which rebuilds all of it from y, z and residual, so that the
+// forward stores nothing for it.
+//
+// Dropout: element e of the (rows, dim) array takes the 16-bit half e % 8 of the
+// four words of Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random
+// numbers: as easy as 1, 2, 3", SC 2011) at counter (e / 8, offset) and key seed,
+// and is kept iff that is at least `drop`, the probability in 65536ths.  The
+// mask is a function of the element, so the gradient makes it again.
+//
+// Bound by HBM: each input read once, each output written once.  A row is held
+// in the registers of its threads, 8 NV values each; the mean of squares is
+// summed by shuffles and, over several waves, through LDS.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "device_common.h"
+#include "ssm_internal.h"
+#include "vec_io.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kMaxWaves = 16;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Keep bits of the eight elements of block `q`, bit j for element 8 q + j.
+__device__ __forceinline__ unsigned keep_bits(uint64_t q, const int64_t* rng, unsigned drop) {
+  const uint64_t seed = (uint64_t)rng[0], offset = (uint64_t)rng[1];
+  unsigned k0 = (unsigned)seed, k1 = (unsigned)(seed >> 32);
+  unsigned c0 = (unsigned)q, c1 = (unsigned)(q >> 32), c2 = (unsigned)offset, c3 = (unsigned)(offset >> 32);
+#pragma unroll
+  for (int round = 0; round < 10; ++round) {
+    const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
+    c0 = (unsigned)(p1 >> 32) ^ c1 ^ k0;
+    c1 = (unsigned)p1;
+    c2 = (unsigned)(p0 >> 32) ^ c3 ^ k1;
+    c3 = (unsigned)p0;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  const unsigned w[4] = {c0, c1, c2, c3};
+  unsigned m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    m |= ((w[j] & 0xffffu) >= drop ? 1u : 0u) << (2 * j);
+    m |= ((w[j] >> 16) >= drop ? 1u : 0u) << (2 * j + 1);
+  }
+  return m;
+}
+
+// Which columns a thread holds: pack j is 8 consecutive columns (VEC), or 8
+// columns tpr apart, each loaded by itself.
+template <bool VEC>
+struct Cols {
+  int tid, tpr;   // thread of the row, threads of a row
+  int64_t dim;
+  __device__ __forceinline__ int64_t at(int j, int e) const {
+    return VEC ? ((int64_t)j * tpr + tid) * 8 + e : ((int64_t)j * 8 + e) * tpr + tid;
+  }
+  __device__ __forceinline__ bool in(int j, int e) const { return at(j, VEC ? 0 : e) < dim; }
+};
+
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load_pack(const void* p, int64_t row, const Cols<VEC>& c, int j, float (&v)[8]) {
+  if constexpr (VEC) {
+    if (c.in(j, 0)) {
+      load8<BF16>(p, row + c.at(j, 0), v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c.in(j, e) ? load1<BF16>(p, row + c.at(j, e)) : 0.f;
+  }
+}
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void store_pack(void* p, int64_t row, const Cols<VEC>& c, int j, const float (&v)[8]) {
+  if constexpr (VEC) {
+    if (c.in(j, 0)) store8<BF16>(p, row + c.at(j, 0), v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c.in(j, e)) store1<BF16>(p, row + c.at(j, e), v[e]);
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ unsigned keep_pack(const NormArgs& a, int64_t row, const Cols<VEC>& c, int j) {
+  if constexpr (VEC) {
+    return keep_bits((uint64_t)(row + c.at(j, 0)) >> 3, a.rng, a.drop);
+  } else {
+    unsigned m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint64_t i = (uint64_t)(row + c.at(j, e));
+      m |= ((keep_bits(i >> 3, a.rng, a.drop) >> (i & 7)) & 1u) << e;
+    }
+    return m;
+  }
+}
+
+// Sums N values over the threads of a row, the same order for every thread.
+// Rows within a wave: shuffles.  Rows of several waves: shuffles, then LDS in the
+// order of the waves (every wave of the workgroup makes the same calls).
+template <int N>
+__device__ __forceinline__ void row_sum(float (&s)[N], int tpr, float (*red)[N], int& buf) {
+  const int top = tpr < 64 ? tpr : 64;
+  for (int sh = 1; sh < top; sh <<= 1)
+#pragma unroll
+    for (int n = 0; n < N; ++n) s[n] += __shfl_xor(s[n], sh);
+  if (tpr > 64) {
+    const int waves = tpr / 64, wave = threadIdx.x >> 6;
+    float(*r)[N] = red + buf * kMaxWaves;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) r[wave][n] = s[n];
+    }
+    lds_sync();
+#pragma unroll
+    for (int n = 0; n < N; ++n) s[n] = 0.f;
+    for (int w = 0; w < waves; ++w)
+#pragma unroll
+      for (int n = 0; n < N; ++n) s[n] += r[w][n];
+    buf ^= 1;   // the next sum writes the other half while slow waves still read this one
+  }
+}
+
+template <bool BF16, bool RBF16, bool VEC, int NV>
+__global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a) {
+  __shared__ float red[2 * kMaxWaves][1];
+  const int rpb = blockDim.x / a.tpr;
+  const int64_t r = (int64_t)blockIdx.x * rpb + threadIdx.x / a.tpr;
+  const bool live = r < a.rows;
+  const Cols<VEC> c{(int)(threadIdx.x % a.tpr), a.tpr, live ? a.dim : 0};
+  const int64_t row = live ? r * a.dim : 0;
+  const float inv = 1.f / (float)a.dim;
+  int buf = 0;
+  float v[NV][8], s[1] = {0.f};
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    load_pack<BF16, VEC>(a.y, row, c, j, v[j]);
+    if (a.z != nullptr) {
+      float z[8];
+      load_pack<BF16, VEC>(a.z, row, c, j, z);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[j][e] *= z[e] * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-z[e] * kLog2e));
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[0] = fmaf(v[j][e], v[j][e], s[0]);
+  }
+  if (a.w_post != nullptr) {
+    row_sum<1>(s, a.tpr, red, buf);
+    const float r1 = __builtin_amdgcn_rsqf(fmaf(s[0], inv, a.eps));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float w[8];
+      load_pack<false, VEC>(a.w_post, 0, c, j, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[j][e] *= r1 * w[e];
+    }
+  }
+  s[0] = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (a.scale != nullptr) {
+      float w[8];
+      load_pack<false, VEC>(a.scale, 0, c, j, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[j][e] *= w[e];
+    }
+    if (a.drop != 0) {
+      const unsigned m = keep_pack<VEC>(a, row, c, j);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[j][e] = (m >> e) & 1u ? v[j][e] * a.keep_scale : 0.f;
+    }
+    if (a.residual != nullptr) {
+      float q[8];
+      load_pack<RBF16, VEC>(a.residual, row, c, j, q);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[j][e] += q[e];
+    }
+    if (a.res_out != nullptr) store_pack<RBF16, VEC>(a.res_out, row, c, j, v[j]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[0] = fmaf(v[j][e], v[j][e], s[0]);
+  }
+  if (a.out != nullptr) {
+    row_sum<1>(s, a.tpr, red, buf);
+    const float r2 = __builtin_amdgcn_rsqf(fmaf(s[0], inv, a.eps));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float w[8];
+      load_pack<false, VEC>(a.w_pre, 0, c, j, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] *= v[j][e] * r2;
+      store_pack<BF16, VEC>(a.out, row, c, j, w);
+    }
+  }
+}
+
+// A pack as it lies in memory, for values that wait while a row is summed.
+template <bool BF16>
+struct Pack {
+  u32x4 u[BF16 ? 1 : 2];
+  __device__ __forceinline__ float get(int e) const {
+    if (BF16) return e % 2 == 0 ? bf16_lo(u[0][e / 2]) : bf16_hi(u[0][e / 2]);
+    const unsigned w = u[BF16 ? 0 : e / 4][e % 4];   // (a scalar first: bit_cast takes no vector element)
+    return __builtin_bit_cast(float, w);
+  }
+};
+template <bool BF16, bool VEC>
+__device__ __forceinline__ Pack<BF16> load_raw(const void* p, int64_t row, const Cols<VEC>& c, int j) {
+  Pack<BF16> r = {};
+  if constexpr (VEC) {
+    if (c.in(j, 0)) {
+      const u32x4* q = reinterpret_cast<const u32x4*>((const char*)p + (row + c.at(j, 0)) * (BF16 ? 2 : 4));
+      r.u[0] = q[0];
+      if (!BF16) r.u[BF16 ? 0 : 1] = q[1];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (c.in(j, e)) {
+        if (BF16) r.u[0][e / 2] |= (unsigned)((const unsigned short*)p)[row + c.at(j, e)] << (16 * (e % 2));
+        else r.u[BF16 ? 0 : e / 4][e % 4] = ((const unsigned*)p)[row + c.at(j, e)];
+      }
+    }
+  }
+  return r;
+}
+
+// Gradient.  With vhat = v / rms(v), Rhat = R / rms(R), q = dout w_pre, w = w_post scale:
+//   dR = dres + (q - Rhat mean(q Rhat)) / rms(R),  dm = dropout(dR),  dn = w dm
+//   dv = (dn - vhat mean(dn vhat)) / rms(v)
+//   dw_post = scale S, dscale = w_post S with S = sum_rows dm vhat;  dw_pre = sum_rows dout Rhat
+// A workgroup walks rows that lie gridDim.x apart and keeps its share of S and
+// dw_pre in registers.
+template <bool BF16, bool RBF16, bool VEC, int NV, int MAXT>
+__global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a) {
+  __shared__ float red1[2 * kMaxWaves][1];
+  __shared__ float red2[2 * kMaxWaves][2];
+  const int rpb = blockDim.x / a.tpr;
+  const int tid = threadIdx.x % a.tpr;
+  const float inv = 1.f / (float)a.dim;
+  int buf1 = 0, buf2 = 0;
+  float gs[NV][8], gpre[NV][8], w[NV][8], wpre[NV][8];
+  {
+    const Cols<VEC> c{tid, a.tpr, a.dim};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        gs[j][e] = gpre[j][e] = wpre[j][e] = 0.f;
+        w[j][e] = 1.f;
+      }
+      if (a.w_post != nullptr) load_pack<false, VEC>(a.w_post, 0, c, j, w[j]);
+      if (a.scale != nullptr) {
+        float sc[8];
+        load_pack<false, VEC>(a.scale, 0, c, j, sc);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[j][e] *= sc[e];
+      }
+      if (a.w_pre != nullptr) load_pack<false, VEC>(a.w_pre, 0, c, j, wpre[j]);
+    }
+  }
+
+  for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < a.rows; r0 += (int64_t)gridDim.x * rpb) {
+    const int64_t r = r0 + threadIdx.x / a.tpr;
+    const bool live = r < a.rows;
+    const Cols<VEC> c{tid, a.tpr, live ? a.dim : 0};
+    const int64_t row = live ? r * a.dim : 0;
+    Pack<BF16> y[NV], z[NV], dout[NV];
+    Pack<RBF16> res[NV], dres[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      y[j] = load_raw<BF16, VEC>(a.y, row, c, j);
+      z[j] = {};
+      res[j] = {};
+      dout[j] = {};
+      dres[j] = {};
+      if (a.z != nullptr) z[j] = load_raw<BF16, VEC>(a.z, row, c, j);
+      if (a.w_pre != nullptr) {
+        if (a.residual != nullptr) res[j] = load_raw<RBF16, VEC>(a.residual, row, c, j);
+        dout[j] = load_raw<BF16, VEC>(a.dout, row, c, j);
+      }
+      if (a.dres != nullptr) dres[j] = load_raw<RBF16, VEC>(a.dres, row, c, j);
+    }
+    float v[NV][8], R[NV][8];   // R: then dn
+    unsigned keep[NV];
+    float s1[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[j][e] = y[j].get(e);
+        if (a.z != nullptr) {
+          const float zz = z[j].get(e);
+          v[j][e] *= zz * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-zz * kLog2e));
+        }
+        s1[0] = fmaf(v[j][e], v[j][e], s1[0]);
+      }
+      keep[j] = a.drop != 0 ? keep_pack<VEC>(a, row, c, j) : 0xffu;
+    }
+    float r1 = 1.f;
+    if (a.w_post != nullptr) {
+      row_sum<1>(s1, a.tpr, red1, buf1);
+      r1 = __builtin_amdgcn_rsqf(fmaf(s1[0], inv, a.eps));
+    }
+    const float rk = r1 * a.keep_scale;
+    float r2 = 0.f, k2 = 0.f;
+    if (a.w_pre != nullptr) {   // R, and with it sum R^2 and sum q R
+      float s2[2] = {0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          R[j][e] = res[j].get(e) + ((keep[j] >> e) & 1u ? v[j][e] * rk * w[j][e] : 0.f);
+          s2[0] = fmaf(R[j][e], R[j][e], s2[0]);
+          s2[1] = fmaf(R[j][e], dout[j].get(e) * wpre[j][e], s2[1]);
+        }
+      row_sum<2>(s2, a.tpr, red2, buf2);
+      r2 = __builtin_amdgcn_rsqf(fmaf(s2[0], inv, a.eps));
+      k2 = s2[1] * inv * r2 * r2;
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) R[j][e] = 0.f;
+    }
+    float s3[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float dR[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = dout[j].get(e);
+        gpre[j][e] = fmaf(d, R[j][e] * r2, gpre[j][e]);
+        dR[e] = fmaf(r2, fmaf(-k2, R[j][e], d * wpre[j][e]), dres[j].get(e));
+      }
+      if (a.dresidual != nullptr) store_pack<RBF16, VEC>(a.dresidual, row, c, j, dR);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float dm = (keep[j] >> e) & 1u ? dR[e] * a.keep_scale : 0.f;
+        gs[j][e] = fmaf(dm, v[j][e] * r1, gs[j][e]);
+        R[j][e] = dm * w[j][e];
+        s3[0] = fmaf(R[j][e], v[j][e], s3[0]);
+      }
+    }
+    float k = 0.f;
+    if (a.w_post != nullptr) {
+      row_sum<1>(s3, a.tpr, red1, buf1);
+      k = s3[0] * inv * r1 * r1;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float dv[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dv[e] = r1 * fmaf(-k, v[j][e], R[j][e]);
+      if (a.z != nullptr) {
+        float dz[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float zz = z[j].get(e);
+          const float sg = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-zz * kLog2e));
+          dz[e] = dv[e] * y[j].get(e) * sg * fmaf(zz, 1.f - sg, 1.f);
+          dv[e] *= zz * sg;
+        }
+        store_pack<BF16, VEC>(a.dz, row, c, j, dz);
+      }
+      store_pack<BF16, VEC>(a.dy, row, c, j, dv);
+    }
+  }
+
+  // rows of the wave, then one part per wave (rows within a wave) or per workgroup
+  for (int sh = a.tpr; sh < 64; sh <<= 1)
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        gs[j][e] += __shfl_xor(gs[j][e], sh);
+        gpre[j][e] += __shfl_xor(gpre[j][e], sh);
+      }
+  const Cols<VEC> c{tid, a.tpr, (int)(threadIdx.x & 63) < a.tpr ? a.dim : 0};
+  const int64_t part = a.tpr <= 64 ? (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6) : blockIdx.x;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    store_pack<false, VEC>(a.ws, part * 2 * a.dim, c, j, gs[j]);
+    store_pack<false, VEC>(a.ws, (part * 2 + 1) * a.dim, c, j, gpre[j]);
+  }
+}
+
+// The weight gradients from the parts of S and dw_pre: 32 columns by 8 slices of the parts.
+__global__ __launch_bounds__(256) void norm_sum_kernel(NormArgs a, int64_t nparts) {
+  __shared__ float red[8][32];
+  const int col = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + col;
+  const int which = blockIdx.y;   // 0: S, 1: dw_pre
+  float s = 0.f;
+  if (c < a.dim)
+    for (int64_t p = slice; p < nparts; p += 8) s += a.ws[(p * 2 + which) * a.dim + c];
+  red[slice][col] = s;
+  lds_sync();
+  if (slice != 0 || c >= a.dim) return;
+  s = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s += red[k][col];
+  if (which == 1) {
+    if (a.dw_pre != nullptr) a.dw_pre[c] = s;
+  } else {
+    if (a.dw_post != nullptr) a.dw_post[c] = a.scale != nullptr ? s * a.scale[c] : s;
+    if (a.dscale != nullptr) a.dscale[c] = a.w_post != nullptr ? s * a.w_post[c] : s;
+  }
+}
+
+// Threads of a row: the fewest that hold it in NV packs of 8 each, a power of two
+// up to a wave, whole waves above.
+int threads_per_row(int64_t dim, int NV) {
+  const int64_t packs = (dim + 8 * NV - 1) / (8 * NV);
+  int t = 8;
+  while (t < 64 && t < packs) t *= 2;
+  return packs <= 64 ? t : (int)((packs + 63) / 64 * 64);
+}
+int packs_fwd(int64_t dim) { return dim <= 8 * 64 ? 1 : 2; }
+int packs_bwd(int64_t dim) { return dim <= 8 * 512 ? 1 : 2; }
+constexpr int64_t kBwdGroups = 512;   // workgroups of the backward at most
+
+struct BwdShape {
+  int NV, tpr, threads;
+  int64_t grid, parts;
+};
+BwdShape bwd_shape(int64_t rows, int64_t dim) {
+  BwdShape s;
+  s.NV = packs_bwd(dim);
+  s.tpr = threads_per_row(dim, s.NV);
+  s.threads = s.tpr <= 64 ? 256 : s.tpr;
+  const int rpb = s.threads / s.tpr;
+  s.grid = std::min<int64_t>(kBwdGroups, (rows + rpb - 1) / rpb);
+  s.parts = s.grid * (s.tpr <= 64 ? s.threads / 64 : 1);
+  return s;
+}
+
+template <bool BF16, bool RBF16>
+void pick_fwd(const NormArgs& a, int NV, unsigned grid, int threads, hipStream_t st) {
+  if (a.vec) {
+    if (NV == 1) norm_fwd_kernel<BF16, RBF16, true, 1><<<grid, threads, 0, st>>>(a);
+    else norm_fwd_kernel<BF16, RBF16, true, 2><<<grid, threads, 0, st>>>(a);
+  } else {
+    if (NV == 1) norm_fwd_kernel<BF16, RBF16, false, 1><<<grid, threads, 0, st>>>(a);
+    else norm_fwd_kernel<BF16, RBF16, false, 2><<<grid, threads, 0, st>>>(a);
+  }
+}
+template <bool BF16, bool RBF16, bool VEC>
+void pick_bwd(const NormArgs& a, const BwdShape& s, hipStream_t st) {
+  const unsigned grid = (unsigned)s.grid;
+  if (s.NV == 1) norm_bwd_kernel<BF16, RBF16, VEC, 1, 512><<<grid, s.threads, 0, st>>>(a);
+  else if (s.threads <= 512) norm_bwd_kernel<BF16, RBF16, VEC, 2, 512><<<grid, s.threads, 0, st>>>(a);
+  else norm_bwd_kernel<BF16, RBF16, VEC, 2, 1024><<<grid, s.threads, 0, st>>>(a);
+}
+template <bool BF16, bool RBF16>
+void pick_bwd(const NormArgs& a, const BwdShape& s, hipStream_t st) {
+  if (a.vec) pick_bwd<BF16, RBF16, true>(a, s, st);
+  else pick_bwd<BF16, RBF16, false>(a, s, st);
+}
+
+}  // namespace
+
+size_t norm_bwd_ws_bytes(int64_t rows, int64_t dim) {
+  return (size_t)bwd_shape(rows, dim).parts * 2 * (size_t)dim * sizeof(float);
+}
+
+int launch_norm_fwd(NormArgs a, void* stream) {
+  hipStream_t st = (hipStream_t)stream;
+  const int NV = packs_fwd(a.dim);
+  a.tpr = threads_per_row(a.dim, NV);
+  const int threads = a.tpr <= 64 ? 256 : a.tpr;
+  const int rpb = threads / a.tpr;
+  const int64_t grid = (a.rows + rpb - 1) / rpb;
+  if (grid > 0x7fffffffLL) return fail(4, "too many rows");
+  if (a.act_bf16) {
+    if (a.res_bf16) pick_fwd<true, true>(a, NV, (unsigned)grid, threads, st);
+    else pick_fwd<true, false>(a, NV, (unsigned)grid, threads, st);
+  } else {
+    if (a.res_bf16) pick_fwd<false, true>(a, NV, (unsigned)grid, threads, st);
+    else pick_fwd<false, false>(a, NV, (unsigned)grid, threads, st);
+  }
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? 0 : fail(6, std::string("block norm launch: ") + hipGetErrorString(e));
+}
+
+int launch_norm_bwd(NormArgs a, void* stream) {
+  hipStream_t st = (hipStream_t)stream;
+  const BwdShape s = bwd_shape(a.rows, a.dim);
+  a.tpr = s.tpr;
+  if (a.rows > 0) {
+    if (a.act_bf16) {
+      if (a.res_bf16) pick_bwd<true, true>(a, s, st);
+      else pick_bwd<true, false>(a, s, st);
+    } else {
+      if (a.res_bf16) pick_bwd<false, true>(a, s, st);
+      else pick_bwd<false, false>(a, s, st);
+    }
+  }
+  if (a.dw_post != nullptr || a.dscale != nullptr || a.dw_pre != nullptr)
+    norm_sum_kernel<<<dim3((unsigned)((a.dim + 31) / 32), 2), 256, 0, st>>>(a, s.parts);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? 0 : fail(6, std::string("block norm backward launch: ") + hipGetErrorString(e));
+}
+
+}  // namespace ssm

@@ -210,6 +210,113 @@ struct ConvArgs {
 
 int launch_conv(const ConvArgs& a, void* stream);
 
+// ---------------------------------------------------------------- causal conv1d backward
+struct ConvBwdArgs {
+  const void* x;
+  const float* w;
+  const float* bias;
+  const void* state_in;
+  const void* dout;
+  const void* dstate_out;  // gradient of the carried-out state, act dtype, or null (zeros)
+  void* dx;
+  float* dweight;          // (dim, width)
+  float* dbias;            // (dim) or null
+  void* dstate_in;         // (batch, dim, width-1) act dtype or null
+  float* ws;               // (nparts, width + 1, dim): the workgroups' shares of dweight and dbias
+  int64_t nparts;          // set by the launch
+  int64_t batch, seqlen, dim, width;
+  int silu;
+  int act_bf16;
+  int vec;                 // 4 channels per thread with 8/16-byte accesses
+};
+
+size_t conv_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int num_cus);
+int launch_conv_bwd(ConvBwdArgs a, int num_cus, void* stream);
+
+// ---------------------------------------------------------------- gated scan
+constexpr int kGatedLru = 0, kGatedUnit = 1;   // enum ssm_gated_form
+constexpr int kGatedSave = 64;                 // tokens between stored states
+constexpr int kGatedMaxCols = 32;              // lanes across channels, at most
+
+struct GatedArgs {
+  const void* x;
+  const void* r;
+  const void* i;               // LRU only
+  const float* A;              // LRU only
+  const unsigned char* reset;  // (batch, seqlen) or null
+  const float* h0;
+  void* y;                     // null: states only
+  float* h_final;
+  float* states;               // (ceil(seqlen / kGatedSave), batch, dim) or null; the state of a single step
+  // backward
+  const float* saved;          // states of the forward
+  const void* dout;
+  const float* dh_final;
+  void* dx;
+  void* dr;
+  void* di;
+  float* dA;
+  float* dh0;
+  // workspace
+  float* ws_h0;                // (batch, dim): state entering the first chunk
+  float* ws_p;                 // (nchunks, batch, dim): maps of the time chunks
+  float* ws_h;
+  float* ws_da;                // (nchunks, batch, dim)
+  int64_t batch, seqlen, dim;
+  int64_t nchunks, chunk_len;
+  int cols;                    // lanes across channels: 4, 8, 16 or 32
+  int form;
+  int act_bf16;
+  int vec;                     // two channels per lane
+};
+
+struct GatedPlan {
+  int cols;
+  int64_t nchunks, chunk_len;
+  size_t maps_bytes, da_bytes, states_bytes;
+};
+GatedPlan plan_gated(int64_t batch, int64_t seqlen, int64_t dim, bool bf16, int num_cus);
+// ws: maps_bytes (forward); maps_bytes + da_bytes, and states_bytes where a.saved is null (backward)
+int launch_gated_fwd(GatedArgs a, const GatedPlan& p, void* ws, void* stream);
+int launch_gated_bwd(GatedArgs a, const GatedPlan& p, void* ws, void* stream);
+int launch_gated_step(const GatedArgs& a, void* stream);
+
+// ---------------------------------------------------------------- block norm
+constexpr int64_t kNormMaxDim = 16384;
+
+struct NormArgs {
+  const void* y;
+  const void* z;            // null: no gate
+  const void* residual;     // null: none
+  const float* w_post;      // null: no norm after the block
+  const float* scale;       // null: 1
+  const float* w_pre;       // null: no norm before the next block
+  const int64_t* rng;       // (seed, offset) on the device; read where drop > 0
+  void* res_out;
+  void* out;
+  // backward
+  const void* dres;
+  const void* dout;
+  void* dy;
+  void* dz;
+  void* dresidual;
+  float* dw_post;
+  float* dscale;
+  float* dw_pre;
+  float* ws;                // (parts, 2, dim)
+  int64_t rows, dim;
+  float eps;
+  float keep_scale;         // 65536 / (65536 - drop)
+  unsigned drop;            // drop probability in 65536ths
+  int act_bf16, res_bf16;
+  int vec;                  // 8 columns per access
+  int tpr;                  // threads of a row (set by the launch)
+};
+
+size_t norm_bwd_ws_bytes(int64_t rows, int64_t dim);
+int launch_norm_fwd(NormArgs a, void* stream);
+int launch_norm_bwd(NormArgs a, void* stream);
+
 int device_cu_count();
 
 }  // namespace ssm
