@@ -591,18 +591,19 @@ static int validate_gated(const void* x, const void* r, const void* i, const flo
 
 size_t ssm_gated_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int act_dtype) {
   if (batch <= 0 || seqlen <= 0 || dim <= 0 || !elems_ok({batch, seqlen, dim})) return 0;
-  return plan_gated(batch, seqlen, dim, act_dtype == SSM_BF16, device_cu_count()).maps_bytes;
+  return plan_gated(batch, seqlen, dim, act_dtype == SSM_BF16, false).words_bytes;
 }
 
 size_t ssm_gated_scan_states_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
   if (batch <= 0 || seqlen <= 0 || dim <= 0 || !elems_ok({batch, seqlen, dim})) return 0;
-  return plan_gated(batch, seqlen, dim, true, device_cu_count()).states_bytes;
+  return plan_gated(batch, seqlen, dim, true, false).states_bytes;
 }
 
 size_t ssm_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int act_dtype, int have_states) {
   if (batch <= 0 || seqlen < 0 || dim <= 0 || !elems_ok({batch, seqlen, dim})) return 0;
-  const GatedPlan p = plan_gated(batch, seqlen, dim, act_dtype == SSM_BF16, device_cu_count());
-  return p.maps_bytes + p.da_bytes + (have_states ? 0 : p.states_bytes);
+  const bool bf16 = act_dtype == SSM_BF16;
+  return gated_bwd_ws_bytes(plan_gated(batch, seqlen, dim, bf16, false), plan_gated(batch, seqlen, dim, bf16, true),
+                            have_states != 0);
 }
 
 int ssm_gated_scan_fwd(const void* x, const void* r, const void* i, const float* A, const uint8_t* reset,
@@ -621,10 +622,10 @@ int ssm_gated_scan_fwd(const void* x, const void* r, const void* i, const float*
   const size_t n = (size_t)(batch * seqlen * dim) * as;
   if (overlap(y, n, x, n) || overlap(y, n, r, n) || overlap(y, n, i, n))
     return fail(SSM_ERR_SHAPE, "y must not overlap an input");
-  const GatedPlan p = plan_gated(batch, seqlen, dim, act_dtype == SSM_BF16, device_cu_count());
+  const GatedPlan p = plan_gated(batch, seqlen, dim, act_dtype == SSM_BF16, false);
   Scratch own;
   void* ws = nullptr;
-  rc = get_workspace(workspace, workspace_bytes, p.maps_bytes, (hipStream_t)stream, &own, &ws);
+  rc = get_workspace(workspace, workspace_bytes, p.words_bytes, (hipStream_t)stream, &own, &ws);
   if (rc != SSM_OK) return rc;
   GatedArgs a{};
   a.x = x; a.r = r; a.i = i; a.A = A; a.reset = reset; a.h0 = h0; a.y = y; a.h_final = h_final; a.states = states;
@@ -656,10 +657,11 @@ int ssm_gated_scan_bwd(const void* x, const void* r, const void* i, const float*
   for (const void* o : out)
     for (const void* q : in)
       if (overlap(o, n, q, n)) return fail(SSM_ERR_SHAPE, "outputs must not overlap inputs");
-  const GatedPlan p = plan_gated(batch, seqlen, dim, act_dtype == SSM_BF16, device_cu_count());
+  const bool bf16 = act_dtype == SSM_BF16;
+  const GatedPlan fwd = plan_gated(batch, seqlen, dim, bf16, false), p = plan_gated(batch, seqlen, dim, bf16, true);
   Scratch own;
   void* ws = nullptr;
-  rc = get_workspace(workspace, workspace_bytes, p.maps_bytes + p.da_bytes + (states != nullptr ? 0 : p.states_bytes),
+  rc = get_workspace(workspace, workspace_bytes, batch > 0 ? gated_bwd_ws_bytes(fwd, p, states != nullptr) : 0,
                      (hipStream_t)stream, &own, &ws);
   if (rc != SSM_OK) return rc;
   GatedArgs a{};
@@ -669,7 +671,7 @@ int ssm_gated_scan_bwd(const void* x, const void* r, const void* i, const float*
   a.vec = dim % 2 == 0;
   for (const void* q : in) a.vec = a.vec && aligned(q, 2 * as);
   for (const void* o : out) a.vec = a.vec && aligned(o, 2 * as);
-  return launch_gated_bwd(a, p, ws, stream);
+  return launch_gated_bwd(a, fwd, p, ws, stream);
 }
 
 int ssm_gated_state_update(const void* x, const void* r, const void* i, const float* A, float* state, void* y,

@@ -7,25 +7,49 @@
 //
 // The map of a run of tokens on the state is affine, h -> P h + H with P the
 // product of its decays, and two runs compose to (P2 P1, P2 H1 + H2).  A
-// workgroup takes a group of channels and walks the sequence in tiles.  Within
-// a tile each lane takes V channels of K consecutive tokens, forms (P, H) of
-// its run in registers, the runs of a wave are combined by shuffles, those of
-// the waves through LDS, and each lane then replays its run from its true
-// starting state.  The gradient runs the tiles from the last to the first: it
-// rebuilds h in the tile from the state stored at the tile's start, and scans
-// the adjoint mu_t = a_t (dout_t + mu_{t+1}) the other way with the same P.
+// workgroup takes a tile, a group of channels by a stretch of time; a lane takes
+// V channels of K consecutive tokens and forms (P, H) of its run in registers;
+// the runs of a wave are combined by shuffles, those of the waves through LDS.
+// The tiles of a channel group are joined on the way: each publishes its map,
+// reads those of the tiles before it back to one whose end state is known,
+// publishes its own end state, and replays its tokens from the state that enters
+// it.  So every input is read once, whatever the lengths and counts are.  The
+// gradient does the same from the last token to the first: it rebuilds h in the
+// tile from the state stored at its start, and joins the adjoint
+// mu_t = a_t (dout_t + mu_{t+1}) with the same P.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "ssm_internal.h"
+#include "vec_io.h"
 
 namespace ssm {
 namespace {
 
-constexpr int kWaves = 8;              // waves of a workgroup
-constexpr int kThreads = 64 * kWaves;
+#ifndef UW
+#define UW 1
+#endif
+#ifndef KF
+#define KF 16
+#endif
+#ifndef KB
+#define KB 8
+#endif
+#ifndef PF
+#define PF 1
+#endif
+#ifndef PB
+#define PB 1
+#endif
+#ifndef WF
+#define WF 1
+#endif
+#ifndef WB
+#define WB 1
+#endif
 constexpr float kLog2e = 1.4426950408889634f;
 // Products of decays are kept from underflowing, so that P == 0 says that the
 // run holds a reset, after which nothing of before (not even a NaN) is left.
@@ -71,48 +95,45 @@ __device__ __forceinline__ float sigmoid(float v) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-v * kLog2e));
 }
 
-// The gates of one element.
-struct Gate {
-  float a;    // decay
-  float s;    // factor of sigma(i) x (LRU) or of x (UNIT)
-  float rs;   // LRU: 1 / s, 0 where s is 0
-  float g;    // LRU: sigma(r)
-};
+// LRU decay of a channel: a = e^la with la = A sigma(r).  a is near 1 and
+// enters a product over thousands of tokens, so it is rounded once from
+// m = 1 - a = -expm1(la), and the same m gives 1 - a^2 = m (1 + a) without
+// cancellation.  Above la = -1/4, m is the series of e^la (the first term left
+// out is under 2^-24 of m); channels with A > -1/4 (FAST) never leave it.
+constexpr float kNear = -0.25f;
+template <bool FAST>
+__device__ __forceinline__ void lru_decay(float la, float& m, float& a) {
+  float p = fmaf(la, -1.f / 720.f, -1.f / 120.f);
+  p = fmaf(p, la, -1.f / 24.f);
+  p = fmaf(p, la, -1.f / 6.f);
+  p = fmaf(p, la, -0.5f);
+  p = fmaf(p, la, -1.f);
+  m = la * p;
+  a = 1.f - m;
+  if (!FAST) {
+    const float e = __builtin_amdgcn_exp2f(la * kLog2e);
+    const bool near1 = la > kNear;
+    m = near1 ? m : 1.f - e;
+    a = near1 ? a : e;
+  }
+}
 
-// LRU decay.  a is near 1 and enters a product over thousands of tokens, so it
-// is rounded once from m = 1 - a = -expm1(la), which below |la| = 1/4 is the
-// series of e^la (the first term left out is under 2^-25 of m); the same m gives
-// 1 - a^2 = m (1 + a) without cancellation.
-__device__ __forceinline__ Gate lru_gate(float r, float A) {
-  Gate q;
-  q.g = sigmoid(r);
-  const float la = A * q.g;
-  const float e = __builtin_amdgcn_exp2f(la * kLog2e);
-  float p = fmaf(la, 1.f / 720.f, 1.f / 120.f);
-  p = fmaf(p, la, 1.f / 24.f);
-  p = fmaf(p, la, 1.f / 6.f);
-  p = fmaf(p, la, 0.5f);
-  p = fmaf(p, la, 1.f);
-  const bool near1 = la > -0.25f;
-  const float m = near1 ? -la * p : 1.f - e;
-  q.a = near1 ? 1.f - m : e;
-  const float w = m * (1.f + q.a);
-  q.rs = w == 0.f ? 0.f : __builtin_amdgcn_rsqf(w);
-  q.s = w * q.rs;
-  return q;
-}
-__device__ __forceinline__ Gate unit_gate(float r) {
-  Gate q;
-  q.a = sigmoid(r);
-  q.s = sigmoid(-r);   // 1 - a without cancellation
-  q.rs = 0.f;
-  q.g = q.a;
-  return q;
-}
-template <int FORM>
-__device__ __forceinline__ Gate gate_of(float r, float A) {
-  if constexpr (FORM == kGatedLru) return lru_gate(r, A);
-  else return unit_gate(r);
+// Decay and input of one element; at a reset a = 0 and the input enters whole.
+template <int FORM, bool FAST, bool RESET>
+__device__ __forceinline__ void gates(float r, float i, float x, float A, bool rs, float& a, float& b) {
+  if constexpr (FORM == kGatedLru) {
+    float m;
+    lru_decay<FAST>(A * sigmoid(r), m, a);
+    float s = __builtin_amdgcn_sqrtf(fmaf(m, a, m));
+    if (RESET) s = rs ? 1.f : s;
+    b = s * (sigmoid(i) * x);
+  } else {
+    a = sigmoid(r);
+    float s = sigmoid(-r);   // 1 - a without cancellation
+    if (RESET) s = rs ? 1.f : s;
+    b = s * x;
+  }
+  if (RESET) a = rs ? 0.f : a;
 }
 
 // (P, H) of an earlier run followed by a later one, into the later one's place.
@@ -132,49 +153,136 @@ __device__ __forceinline__ float after(float p, float h, float state) {
   return RESET && p == 0.f ? h : fmaf(p, state, h);
 }
 
-// Where a workgroup and a lane stand.  Workgroups of neighbouring channel
-// groups run on one XCD (workgroup ids go round the 8 XCDs), so that the lines
-// they share are read into one L2.
+// Where a workgroup and a lane stand.  Tiles are taken in the order of a
+// counter, channel groups fastest and time last (from the end for the
+// gradient), so that the tiles a workgroup waits for have all been taken by
+// workgroups that run.
 struct Place {
   int col, row, wave, lane;
-  int64_t b, c0, chunk, t_begin, t_end;
+  int64_t b, c0, tile, t0;
   bool active;
 };
-template <int V>
-__device__ __forceinline__ Place place(const GatedArgs& a) {
+template <int V, int DIR>
+__device__ __forceinline__ Place place(const GatedArgs& a, int64_t T) {
+  __shared__ unsigned taken;
   Place p;
-  const unsigned n = gridDim.x, q = n / 8, rest = n % 8, xcd = blockIdx.x % 8;
-  const unsigned id = xcd * q + (xcd < rest ? xcd : rest) + blockIdx.x / 8;
+  unsigned id = blockIdx.x;
+  if (a.ntiles > 1) {
+    if (threadIdx.x == 0) taken = atomicAdd(a.ws_count, 1u);
+    lds_sync();
+    id = __builtin_amdgcn_readfirstlane(taken);
+  }
   const int64_t cw = (int64_t)a.cols * V;
   const unsigned groups = (unsigned)((a.dim + cw - 1) / cw);
-  const unsigned rest2 = id / groups;
+  const unsigned rest = id / groups;
   p.lane = threadIdx.x & 63;
   p.wave = threadIdx.x >> 6;
   p.col = p.lane & (a.cols - 1);
   p.row = p.wave * (64 / a.cols) + p.lane / a.cols;
-  p.b = rest2 % (unsigned)a.batch;
-  p.chunk = rest2 / (unsigned)a.batch;
+  p.b = rest % (unsigned)a.batch;
+  p.tile = rest / (unsigned)a.batch;
+  if (DIR < 0) p.tile = a.ntiles - 1 - p.tile;
+  p.t0 = p.tile * T;
   p.c0 = (int64_t)(id % groups) * cw + p.col * V;
   p.active = p.c0 < a.dim;
-  p.t_begin = p.chunk * a.chunk_len;
-  p.t_end = min(a.seqlen, p.t_begin + a.chunk_len);
   return p;
 }
 
-// K tokens of one lane, from a uniform address and the lane's byte offset; the
-// tokens from nv on are left as they are.
-template <bool BF16, int V, int K>
-__device__ __forceinline__ void load_run(const void* src, int64_t first, int64_t dim, unsigned off, int nv,
+// What a tile publishes per channel, in one 64-bit word each, so that no order
+// between words is asked for: its map (P in the high half; never the all-ones
+// that the words are cleared to, since P is no NaN), then its end state (0 in
+// the high half).
+constexpr unsigned kUnset = 0xffffffffu;
+__device__ __forceinline__ uint64_t word(unsigned hi, float lo) {
+  return ((uint64_t)hi << 32) | __builtin_bit_cast(unsigned, lo);
+}
+__device__ __forceinline__ void publish(uint64_t* p, uint64_t v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t look(const uint64_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float low(uint64_t w) { return __builtin_bit_cast(float, (unsigned)w); }
+__device__ __forceinline__ unsigned high(uint64_t w) { return (unsigned)(w >> 32); }
+
+// The state that enters a tile from the `before` tiles before it in the order
+// of the scan, for one channel a lane, called by one whole wave.  at(k) is the
+// place of the k-th tile before (k from 1).  The state is always folded tile
+// after tile from a known end state, which itself was folded so: the same
+// bits, whatever tile the fold starts from.  It waits only for maps, which
+// every tile publishes before it waits for anything, and for the first tile's
+// end state, which waits for nothing.
+constexpr int kAhead = 8;   // words read at a time
+template <bool RESET, class At>
+__device__ __forceinline__ float entering(const uint64_t* maps, const uint64_t* ends, int64_t before, At at, bool on) {
+  // the nearest tile with a known end state
+  int64_t k = 1;
+  uint64_t w[kAhead];
+  float h = 0.f;
+  for (bool found = false; !found;) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) w[j] = on && k + j <= before ? look(ends + at(k + j)) : 0;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (!found && k + j <= before && __all(high(w[j]) == 0)) {
+        found = true;
+        h = low(w[j]);
+        k += j;
+        break;
+      }
+    }
+    if (!found) {
+      k = k + kAhead <= before ? k + kAhead : before;   // in the end the first tile's, which is waited for
+      if (k == before) __builtin_amdgcn_s_sleep(1);
+    }
+  }
+  // the maps from there to this tile
+  for (--k; k > 0;) {
+    const int n = k < kAhead ? (int)k : kAhead;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) w[j] = on && j < n ? look(maps + at(k - j)) : 0;
+    int done = 0;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (j < n && done == j && __all(high(w[j]) != kUnset)) {
+        h = after<RESET>(__builtin_bit_cast(float, high(w[j])), low(w[j]), h);
+        done = j + 1;
+      }
+    }
+    k -= done;
+    if (done == 0) __builtin_amdgcn_s_sleep(1);
+  }
+  return h;
+}
+
+// K tokens of one lane, from element `first` on: the tile's address in scalar
+// registers, the lane's byte offset in a vector register, the token's in a
+// scalar one (a buffer access; with plain addresses the compiler adds the token
+// to the lane's offset, a vector instruction for each).  The tokens from nv on
+// are left alone.  FULL: nv is K.
+constexpr int kBufferFlags = 0x00027000;   // raw 32-bit elements
+template <bool BF16, int V, int K, bool FULL>
+__device__ __forceinline__ void load_run(const void* src, int64_t first, unsigned step, unsigned off, int nv,
                                          Raw<BF16, V> (&out)[K]) {
-  const char* base = (const char*)src + first * (BF16 ? 2 : 4);
-  const int64_t step = dim * (BF16 ? 2 : 4);
-  if (nv == K) {
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((char*)src + first * (BF16 ? 2 : 4), 0, 0x7fffffff, kBufferFlags);
 #pragma unroll
-    for (int j = 0; j < K; ++j) out[j] = *reinterpret_cast<const Raw<BF16, V>*>(base + j * step + off);
-  } else {
+  for (int j = 0; j < K; ++j) {
+    if (!FULL && j >= nv) continue;
+    if constexpr (sizeof(out[j]) == 2) out[j] = __builtin_bit_cast(Raw<BF16, V>, __builtin_amdgcn_raw_buffer_load_b16(rsrc, off, j * step, 0));
+    else if constexpr (sizeof(out[j]) == 4) out[j] = __builtin_bit_cast(Raw<BF16, V>, __builtin_amdgcn_raw_buffer_load_b32(rsrc, off, j * step, 0));
+    else out[j] = __builtin_bit_cast(Raw<BF16, V>, __builtin_amdgcn_raw_buffer_load_b64(rsrc, off, j * step, 0));
+  }
+}
+template <bool BF16, int V, int K, bool FULL>
+__device__ __forceinline__ void store_run(void* dst, int64_t first, unsigned step, unsigned off, int nv,
+                                          const Raw<BF16, V> (&v)[K]) {
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((char*)dst + first * (BF16 ? 2 : 4), 0, 0x7fffffff, kBufferFlags);
 #pragma unroll
-    for (int j = 0; j < K; ++j)
-      if (j < nv) out[j] = *reinterpret_cast<const Raw<BF16, V>*>(base + j * step + off);
+  for (int j = 0; j < K; ++j) {
+    if (!FULL && j >= nv) continue;
+    if constexpr (sizeof(v[j]) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v[j]), rsrc, off, j * step, 0);
+    else if constexpr (sizeof(v[j]) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v[j]), rsrc, off, j * step, 0);
+    else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v[j]), rsrc, off, j * step, 0);
   }
 }
 
@@ -218,359 +326,333 @@ __device__ __forceinline__ void wave_scan(int lane, int cols, float (&p)[V], flo
   }
 }
 
-// Forward.  AGG: only the map of each time chunk, (ws_p, ws_h), for chunks that
-// run in parallel; else y, the states entering every kGatedSave-th token and
-// the final state, from the maps of the chunks before.
-template <bool BF16, int V, int FORM, bool RESET, int K, bool AGG>
-__global__ __launch_bounds__(kThreads) void gated_fwd_kernel(GatedArgs a) {
-  __shared__ float2 tot[2][kWaves][kGatedMaxCols][V];
-  const Place q = place<V>(a);
-  const int R = 64 / a.cols;
-  const int T = kWaves * R * K;
+// Forward: y, the states entering every kGatedSave-th token and the final state.
+template <bool BF16, int V, int FORM, bool RESET, int K, int NW>
+__global__ __launch_bounds__(64 * NW) void gated_fwd_kernel(GatedArgs a) {
+  __shared__ float2 tot[NW][kGatedMaxCols * V];
+  __shared__ float enter[kGatedMaxCols * V];
+  const int T = NW * (64 / a.cols) * K;
+  const Place q = place<V, 1>(a, T);
   const int64_t L = a.seqlen, dim = a.dim;
   const int64_t plane = a.batch * dim;
   const int64_t state_at = q.b * dim + q.c0;   // (b, c0)
   const unsigned es = BF16 ? 2 : 4;
   const int64_t c_ld = q.active ? q.c0 : 0;
-  const unsigned off = (unsigned)(((int64_t)q.row * K * dim + c_ld) * es);
+  const unsigned off = (unsigned)(((int64_t)q.row * K * dim + c_ld) * es), step = (unsigned)dim * es;
+  const int64_t first = (q.b * L + q.t0) * dim, tl = q.t0 + q.row * K;
 
-  float A[V], carry[V], pall[V];
+  float A[V];
+  bool near1 = true;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     A[v] = FORM == kGatedLru ? a.A[c_ld + v] : 0.f;
-    carry[v] = 0.f;
-    pall[v] = 1.f;
-    if (!AGG && q.active) {
-      if (a.nchunks > 1) {   // the state entering the first chunk, then the chunks before this one
-        carry[v] = a.ws_h0[state_at + v];
-        for (int64_t k = 0; k < q.chunk; ++k)
-          carry[v] = after<RESET>(a.ws_p[k * plane + state_at + v], a.ws_h[k * plane + state_at + v], carry[v]);
-      } else if (a.h0 != nullptr) {
-        carry[v] = a.h0[state_at + v];
-      }
-    }
-  }
-  if (AGG && q.chunk == 0 && q.active && q.row == 0) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) a.ws_h0[state_at + v] = a.h0 != nullptr ? a.h0[state_at + v] : 0.f;
+    near1 = near1 && A[v] > kNear;
   }
 
-  int buf = 0;
-  for (int64_t t0 = q.t_begin; t0 < q.t_end; t0 += T, buf ^= 1) {
-    const int64_t tl = t0 + q.row * K;
-    const int nv = (int)max((int64_t)0, min((int64_t)K, q.t_end - tl));
-    const int64_t first = (q.b * L + t0) * dim;
-    Raw<BF16, V> rr[K] = {}, ri[K] = {}, rx[K] = {};
-    load_run<BF16, V, K>(a.r, first, dim, off, nv, rr);
-    if (FORM == kGatedLru) load_run<BF16, V, K>(a.i, first, dim, off, nv, ri);
-    load_run<BF16, V, K>(a.x, first, dim, off, nv, rx);
-    const unsigned rm = RESET ? load_resets<K>(a.reset, q.b * L + tl, nv) : 0u;
-
+  // FF: a whole tile, and every decay near 1
+  auto run = [&](auto fast_full) {
+    constexpr bool FF = decltype(fast_full)::value;
+    const int nv = FF ? K : (int)max((int64_t)0, min((int64_t)K, L - tl));
     float da[K][V], db[K][V], p[V], h[V];
+    unsigned resets = 0;
+    {
+      Raw<BF16, V> rr[K], ri[K], rx[K];
+      if (!FF)
 #pragma unroll
-    for (int v = 0; v < V; ++v) { p[v] = 1.f; h[v] = 0.f; }
+        for (int j = 0; j < K; ++j) { rr[j] = {}; ri[j] = {}; rx[j] = {}; }
+      load_run<BF16, V, K, FF>(a.r, first, step, off, nv, rr);
+      if (FORM == kGatedLru) load_run<BF16, V, K, FF>(a.i, first, step, off, nv, ri);
+      load_run<BF16, V, K, FF>(a.x, first, step, off, nv, rx);
+      if (RESET) resets = load_resets<K>(a.reset, q.b * L + tl, nv);
 #pragma unroll
-    for (int j = 0; j < K; ++j) {
-      const bool rs = RESET && ((rm >> j) & 1u);
+      for (int v = 0; v < V; ++v) { p[v] = 1.f; h[v] = 0.f; }
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        Gate w = gate_of<FORM>(rr[j].get(v), A[v]);
-        if (RESET) { w.a = rs ? 0.f : w.a; w.s = rs ? 1.f : w.s; }
-        float u = rx[j].get(v);
-        if (FORM == kGatedLru) u *= sigmoid(ri[j].get(v));
-        const bool in = j < nv;
-        da[j][v] = in ? w.a : 1.f;
-        db[j][v] = in ? w.s * u : 0.f;
-        h[v] = rs ? db[j][v] : fmaf(da[j][v], h[v], db[j][v]);
-        p[v] *= da[j][v];
+      for (int j = 0; j < K; ++j) {
+        const bool rs = RESET && ((resets >> j) & 1u);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          gates<FORM, FF, RESET>(rr[j].get(v), FORM == kGatedLru ? ri[j].get(v) : 0.f, rx[j].get(v), A[v], rs, da[j][v],
+                                 db[j][v]);
+          if (!FF) {
+            da[j][v] = j < nv ? da[j][v] : 1.f;
+            db[j][v] = j < nv ? db[j][v] : 0.f;
+          }
+          h[v] = rs ? db[j][v] : fmaf(da[j][v], h[v], db[j][v]);
+          p[v] *= da[j][v];
+        }
       }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) p[v] = RESET && rm != 0 ? 0.f : fmaxf(p[v], kTinyP);
-
+    for (int v = 0; v < V; ++v) p[v] = RESET && resets != 0 ? 0.f : fmaxf(p[v], kTinyP);
     float pe[V], he[V];
     wave_scan<RESET, 1, V>(q.lane, a.cols, p, h, pe, he);
     if (q.lane >= 64 - a.cols) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) tot[buf][q.wave][q.col][v] = make_float2(p[v], h[v]);
+      for (int v = 0; v < V; ++v) tot[q.wave][q.col * V + v] = make_float2(p[v], h[v]);
+    }
+    lds_sync();
+    if (q.wave == 0) {   // one channel a lane
+      const int64_t c = q.c0 - q.col * V + q.lane;
+      const bool on = q.lane < a.cols * V && c < dim;
+      const int64_t at = q.b * dim + (on ? c : 0);
+      float pt = 1.f, ht = 0.f;
+      for (int w = 0; w < NW; ++w) {
+        const float2 f = tot[w][on ? q.lane : 0];
+        float p2 = f.x, h2 = f.y;
+        then<RESET>(pt, ht, p2, h2);
+        pt = p2; ht = h2;
+      }
+      const int64_t slot = q.tile * plane + at;
+      if (on && a.ntiles > 1) publish(a.ws_maps + slot, word(__builtin_bit_cast(unsigned, pt), ht));
+      float hin = 0.f;
+      if (q.tile > 0) hin = entering<RESET>(a.ws_maps, a.ws_ends, q.tile, [&](int64_t k) { return slot - k * plane; }, on);
+      else if (on && a.h0 != nullptr) hin = a.h0[at];
+      const float hout = after<RESET>(pt, ht, hin);
+      if (on) {
+        if (a.ntiles > 1) publish(a.ws_ends + slot, word(0, hout));
+        if (a.h_final != nullptr && q.tile == a.ntiles - 1) a.h_final[at] = hout;
+        enter[q.lane] = hin;
+      }
     }
     lds_sync();
     float st[V];
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+    for (int v = 0; v < V; ++v) st[v] = enter[q.col * V + v];
+    for (int w = 0; w < q.wave; ++w)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float2 ph = tot[buf][w][q.col][v];
-        if (w == q.wave) st[v] = carry[v];
-        carry[v] = after<RESET>(ph.x, ph.y, carry[v]);
-        if (AGG) pall[v] = RESET && (pall[v] == 0.f || ph.x == 0.f) ? 0.f : fmaxf(pall[v] * ph.x, kTinyP);
+        const float2 f = tot[w][q.col * V + v];
+        st[v] = after<RESET>(f.x, f.y, st[v]);
       }
+#pragma unroll
+    for (int v = 0; v < V; ++v) st[v] = after<RESET>(pe[v], he[v], st[v]);
+    if (a.states != nullptr && (q.row * K) % kGatedSave == 0 && nv > 0 && q.active) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) a.states[(tl / kGatedSave) * plane + state_at + v] = st[v];
     }
-    if (!AGG) {
+    if (a.y == nullptr) return;
+    Raw<BF16, V> out[K];
 #pragma unroll
-      for (int v = 0; v < V; ++v) st[v] = after<RESET>(pe[v], he[v], st[v]);
-      if (a.states != nullptr && (q.row * K) % kGatedSave == 0 && nv > 0 && q.active) {
+    for (int j = 0; j < K; ++j) {
+      const bool rs = RESET && ((resets >> j) & 1u);
 #pragma unroll
-        for (int v = 0; v < V; ++v) a.states[(tl / kGatedSave) * plane + state_at + v] = st[v];
-      }
-      char* yb = (char*)a.y + first * es;
+      for (int v = 0; v < V; ++v) st[v] = rs ? db[j][v] : fmaf(da[j][v], st[v], db[j][v]);
+      out[j] = Raw<BF16, V>::make(st);
+    }
+    if (q.active) store_run<BF16, V, K, FF>(a.y, first, step, off, nv, out);
+  };
+  if ((FORM != kGatedLru || __all(near1)) && q.t0 + T <= L) run(std::true_type{});
+  else run(std::false_type{});
+}
+
+// Hides where a value comes from, so that what is formed from it again is
+// formed again and not kept in registers from the first time.
+__device__ __forceinline__ void forget(float& v) { asm volatile("" : "+v"(v)); }
+
+// Backward: dx, dr, di, dh0 and the tile's share of dA.  The sigmoids are formed
+// once and kept; decay and root are formed from them for the scans, and again
+// for the gradients (13 instructions) instead of waiting in registers.
+template <bool BF16, int V, int FORM, bool RESET, int K, int NW>
+__global__ __launch_bounds__(64 * NW) void gated_bwd_kernel(GatedArgs a) {
+  __shared__ float2 tot[NW][kGatedMaxCols * V];   // (P, H) of the waves' runs
+  __shared__ float tom[NW][kGatedMaxCols * V];    // M of the waves' runs
+  __shared__ float enter[kGatedMaxCols * V];
+  const int T = NW * (64 / a.cols) * K;
+  const Place q = place<V, -1>(a, T);
+  const int64_t L = a.seqlen, dim = a.dim;
+  const int64_t plane = a.batch * dim;
+  const int64_t state_at = q.b * dim + q.c0;
+  const unsigned es = BF16 ? 2 : 4;
+  const int64_t c_ld = q.active ? q.c0 : 0;
+  const unsigned off = (unsigned)(((int64_t)q.row * K * dim + c_ld) * es), step = (unsigned)dim * es;
+  const int64_t first = (q.b * L + q.t0) * dim, tl = q.t0 + q.row * K;
+  float A[V], accA[V];
+  bool near1 = true;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    A[v] = FORM == kGatedLru ? a.A[c_ld + v] : 0.f;
+    near1 = near1 && A[v] > kNear;
+    accA[v] = 0.f;
+  }
+
+  // FF: a whole tile, and every decay near 1
+  auto run = [&](auto fast_full) {
+    constexpr bool FF = decltype(fast_full)::value;
+    const int nv = FF ? K : (int)max((int64_t)0, min((int64_t)K, L - tl));
+    float g[K][V], gi[K][V], hp[K][V], ms[V], st[V];
+    Raw<BF16, V> rx[K], rd[K];
+    unsigned resets = 0;
+    {
+      Raw<BF16, V> rr[K], ri[K];
+      if (!FF)
+#pragma unroll
+        for (int j = 0; j < K; ++j) { rr[j] = {}; ri[j] = {}; rx[j] = {}; rd[j] = {}; }
+      load_run<BF16, V, K, FF>(a.r, first, step, off, nv, rr);
+      if (FORM == kGatedLru) load_run<BF16, V, K, FF>(a.i, first, step, off, nv, ri);
+      load_run<BF16, V, K, FF>(a.x, first, step, off, nv, rx);
+      load_run<BF16, V, K, FF>(a.dout, first, step, off, nv, rd);
+      if (RESET) resets = load_resets<K>(a.reset, q.b * L + tl, nv);
+#pragma unroll
+      for (int v = 0; v < V; ++v) st[v] = L > 0 ? a.saved[(q.t0 / kGatedSave) * plane + q.b * dim + c_ld + v] : 0.f;
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          g[j][v] = sigmoid(rr[j].get(v));
+          gi[j][v] = FORM == kGatedLru ? sigmoid(ri[j].get(v)) : sigmoid(-rr[j].get(v));   // UNIT: 1 - a
+        }
+    }
+    {
+      float da[K][V], p[V], h[V], m[V], pr[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) { p[v] = 1.f; h[v] = 0.f; m[v] = 0.f; }
 #pragma unroll
       for (int j = 0; j < K; ++j) {
-        const bool rs = RESET && ((rm >> j) & 1u);
+        const bool rs = RESET && ((resets >> j) & 1u);
 #pragma unroll
-        for (int v = 0; v < V; ++v) st[v] = rs ? db[j][v] : fmaf(da[j][v], st[v], db[j][v]);
-        if (a.y != nullptr && j < nv && q.active)
-          *reinterpret_cast<Raw<BF16, V>*>(yb + j * dim * es + off) = Raw<BF16, V>::make(st);
-      }
-    }
-  }
-  if (AGG) {
-    if (q.active && q.row == 0) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        a.ws_p[q.chunk * plane + state_at + v] = pall[v];
-        a.ws_h[q.chunk * plane + state_at + v] = carry[v];
-      }
-    }
-  } else if (a.h_final != nullptr && q.chunk == a.nchunks - 1) {
-    __syncthreads();   // with no token, every wave has read h0, which h_final may be
-    if (q.active && q.row == 0) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) a.h_final[state_at + v] = carry[v];
-    }
-  }
-}
-
-// Backward of a time chunk from what later chunks hand back: the map of mu
-// over the chunk, for chunks that run in parallel.
-template <bool BF16, int V, int FORM, bool RESET, int K>
-__global__ __launch_bounds__(kThreads) void gated_bwd_agg_kernel(GatedArgs a) {
-  __shared__ float2 tot[2][kWaves][kGatedMaxCols][V];
-  const Place q = place<V>(a);
-  const int T = kWaves * (64 / a.cols) * K;
-  const int64_t L = a.seqlen, dim = a.dim;
-  const int64_t plane = a.batch * dim;
-  const int64_t state_at = q.b * dim + q.c0;
-  const unsigned es = BF16 ? 2 : 4;
-  const int64_t c_ld = q.active ? q.c0 : 0;
-  const unsigned off = (unsigned)(((int64_t)q.row * K * dim + c_ld) * es);
-  float A[V], carry[V], pall[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    A[v] = FORM == kGatedLru ? a.A[c_ld + v] : 0.f;
-    carry[v] = 0.f;
-    pall[v] = 1.f;
-  }
-  int buf = 0;
-  const int64_t ntiles = (q.t_end - q.t_begin + T - 1) / T;
-  for (int64_t it = ntiles - 1; it >= 0; --it, buf ^= 1) {
-    const int64_t t0 = q.t_begin + it * T, tl = t0 + q.row * K;
-    const int nv = (int)max((int64_t)0, min((int64_t)K, q.t_end - tl));
-    const int64_t first = (q.b * L + t0) * dim;
-    Raw<BF16, V> rr[K] = {}, rd[K] = {};
-    load_run<BF16, V, K>(a.r, first, dim, off, nv, rr);
-    load_run<BF16, V, K>(a.dout, first, dim, off, nv, rd);
-    const unsigned rm = RESET ? load_resets<K>(a.reset, q.b * L + tl, nv) : 0u;
-    float p[V], m[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) { p[v] = 1.f; m[v] = 0.f; }
-#pragma unroll
-    for (int j = K - 1; j >= 0; --j) {
-      const bool rs = RESET && ((rm >> j) & 1u);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const Gate w = gate_of<FORM>(rr[j].get(v), A[v]);
-        const bool in = j < nv;
-        const float lam = m[v] + (in ? rd[j].get(v) : 0.f);
-        m[v] = rs ? 0.f : (in ? w.a * lam : lam);
-        p[v] *= in ? w.a : 1.f;
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) p[v] = RESET && rm != 0 ? 0.f : fmaxf(p[v], kTinyP);
-    float pe[V], me[V];
-    wave_scan<RESET, -1, V>(q.lane, a.cols, p, m, pe, me);
-    if (q.lane < a.cols) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) tot[buf][q.wave][q.col][v] = make_float2(p[v], m[v]);
-    }
-    lds_sync();
-#pragma unroll
-    for (int w = kWaves - 1; w >= 0; --w) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float2 ph = tot[buf][w][q.col][v];
-        carry[v] = after<RESET>(ph.x, ph.y, carry[v]);
-        pall[v] = RESET && (pall[v] == 0.f || ph.x == 0.f) ? 0.f : fmaxf(pall[v] * ph.x, kTinyP);
-      }
-    }
-  }
-  if (q.active && q.row == 0) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      a.ws_p[q.chunk * plane + state_at + v] = pall[v];
-      a.ws_h[q.chunk * plane + state_at + v] = carry[v];
-    }
-  }
-}
-
-// Backward: dx, dr, di, dh0 and the workgroup's share of dA.
-template <bool BF16, int V, int FORM, bool RESET, int K>
-__global__ __launch_bounds__(kThreads) void gated_bwd_kernel(GatedArgs a) {
-  __shared__ float2 tot[2][kWaves][kGatedMaxCols][V];   // (P, H) of the waves' runs
-  __shared__ float tom[2][kWaves][kGatedMaxCols][V];    // M of the waves' runs
-  const Place q = place<V>(a);
-  const int T = kWaves * (64 / a.cols) * K;
-  const int64_t L = a.seqlen, dim = a.dim;
-  const int64_t plane = a.batch * dim;
-  const int64_t state_at = q.b * dim + q.c0;
-  const unsigned es = BF16 ? 2 : 4;
-  const int64_t c_ld = q.active ? q.c0 : 0;
-  const unsigned off = (unsigned)(((int64_t)q.row * K * dim + c_ld) * es);
-  float A[V], mu[V], accA[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    A[v] = FORM == kGatedLru ? a.A[c_ld + v] : 0.f;
-    mu[v] = a.dh_final != nullptr && q.active ? a.dh_final[state_at + v] : 0.f;
-    accA[v] = 0.f;
-    if (q.active)
-      for (int64_t k = a.nchunks - 1; k > q.chunk; --k)
-        mu[v] = after<RESET>(a.ws_p[k * plane + state_at + v], a.ws_h[k * plane + state_at + v], mu[v]);
-  }
-  int buf = 0;
-  const int64_t ntiles = (q.t_end - q.t_begin + T - 1) / T;
-  for (int64_t it = ntiles - 1; it >= 0; --it, buf ^= 1) {
-    const int64_t t0 = q.t_begin + it * T, tl = t0 + q.row * K;
-    const int nv = (int)max((int64_t)0, min((int64_t)K, q.t_end - tl));
-    const int64_t first = (q.b * L + t0) * dim;
-    Raw<BF16, V> rr[K] = {}, ri[K] = {}, rx[K] = {}, rd[K] = {};
-    load_run<BF16, V, K>(a.r, first, dim, off, nv, rr);
-    if (FORM == kGatedLru) load_run<BF16, V, K>(a.i, first, dim, off, nv, ri);
-    load_run<BF16, V, K>(a.x, first, dim, off, nv, rx);
-    load_run<BF16, V, K>(a.dout, first, dim, off, nv, rd);
-    const unsigned rm = RESET ? load_resets<K>(a.reset, q.b * L + tl, nv) : 0u;
-    float hst[V];   // the state entering the tile
-#pragma unroll
-    for (int v = 0; v < V; ++v) hst[v] = q.active ? a.saved[(t0 / kGatedSave) * plane + state_at + v] : 0.f;
-
-    float da[K][V], hp[K][V], p[V], h[V], m[V], pr[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) { p[v] = 1.f; h[v] = 0.f; m[v] = 0.f; }
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-      const bool rs = RESET && ((rm >> j) & 1u);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        Gate w = gate_of<FORM>(rr[j].get(v), A[v]);
-        if (RESET) { w.a = rs ? 0.f : w.a; w.s = rs ? 1.f : w.s; }
-        float u = rx[j].get(v);
-        if (FORM == kGatedLru) u *= sigmoid(ri[j].get(v));
-        const bool in = j < nv;
-        da[j][v] = in ? w.a : 1.f;
-        hp[j][v] = in ? w.s * u : 0.f;   // b, replaced by h_{t-1} below
-        h[v] = rs ? hp[j][v] : fmaf(da[j][v], h[v], hp[j][v]);
-        p[v] *= da[j][v];
-      }
-    }
-#pragma unroll
-    for (int j = K - 1; j >= 0; --j) {
-      const bool rs = RESET && ((rm >> j) & 1u);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float lam = m[v] + (j < nv ? rd[j].get(v) : 0.f);
-        m[v] = rs ? 0.f : da[j][v] * lam;
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      p[v] = RESET && rm != 0 ? 0.f : fmaxf(p[v], kTinyP);
-      pr[v] = p[v];
-    }
-    float pe[V], he[V], qe[V], me[V];
-    wave_scan<RESET, 1, V>(q.lane, a.cols, p, h, pe, he);
-    wave_scan<RESET, -1, V>(q.lane, a.cols, pr, m, qe, me);
-    if (q.lane >= 64 - a.cols) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) tot[buf][q.wave][q.col][v] = make_float2(p[v], h[v]);
-    }
-    if (q.lane < a.cols) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) tom[buf][q.wave][q.col][v] = m[v];
-    }
-    lds_sync();
-    float st[V], ms[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) { st[v] = hst[v]; ms[v] = mu[v]; }
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float2 f = tot[buf][w][q.col][v];
-        if (w < q.wave) st[v] = after<RESET>(f.x, f.y, st[v]);
-        const int w2 = kWaves - 1 - w;
-        const float2 f2 = tot[buf][w2][q.col][v];
-        if (w2 == q.wave) ms[v] = mu[v];
-        mu[v] = after<RESET>(f2.x, tom[buf][w2][q.col][v], mu[v]);
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      st[v] = after<RESET>(pe[v], he[v], st[v]);
-      ms[v] = after<RESET>(qe[v], me[v], ms[v]);
-    }
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-      const bool rs = RESET && ((rm >> j) & 1u);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float b = hp[j][v];
-        hp[j][v] = st[v];
-        st[v] = rs ? b : fmaf(da[j][v], st[v], b);
-      }
-    }
-    char* xb = (char*)a.dx + first * es;
-    char* gb = (char*)a.dr + first * es;
-    char* ib = (char*)a.di + first * es;
-#pragma unroll
-    for (int j = K - 1; j >= 0; --j) {
-      const bool rs = RESET && ((rm >> j) & 1u);
-      float ox[V], og[V], oi[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const bool in = j < nv;
-        const float lam = ms[v] + (in ? rd[j].get(v) : 0.f);
-        const float x = rx[j].get(v);
-        Gate w = gate_of<FORM>(rr[j].get(v), A[v]);
-        if (RESET) w.s = rs ? 1.f : w.s;
-        if constexpr (FORM == kGatedLru) {
-          const float gi = sigmoid(ri[j].get(v));
-          const float u = gi * x, ls = lam * w.s;
-          float dla = lam * w.a * fmaf(-u * w.a, w.rs, hp[j][v]);
-          if (RESET) dla = rs ? 0.f : dla;
-          const float dag = dla * w.g;
-          accA[v] += in ? dag : 0.f;
-          og[v] = dag * A[v] * (1.f - w.g);
-          ox[v] = ls * gi;
-          oi[v] = ls * u * (1.f - gi);
-        } else {
-          ox[v] = lam * w.s;
-          og[v] = rs ? 0.f : ox[v] * w.a * (hp[j][v] - x);
-          oi[v] = 0.f;
+        for (int v = 0; v < V; ++v) {
+          const float x = rx[j].get(v);
+          float dec = g[j][v], b = gi[j][v] * x;
+          if constexpr (FORM == kGatedLru) {
+            float mm;
+            lru_decay<FF>(A[v] * g[j][v], mm, dec);
+            float s = __builtin_amdgcn_sqrtf(fmaf(mm, dec, mm));
+            if (RESET) s = rs ? 1.f : s;
+            b *= s;
+          } else if (RESET) {
+            b = rs ? x : b;
+          }
+          if (RESET) dec = rs ? 0.f : dec;
+          if (!FF) {
+            dec = j < nv ? dec : 1.f;
+            b = j < nv ? b : 0.f;
+          }
+          da[j][v] = dec;
+          hp[j][v] = b;   // replaced by h_{t-1} below
+          h[v] = rs ? b : fmaf(dec, h[v], b);
+          p[v] *= dec;
         }
-        ms[v] = rs ? 0.f : da[j][v] * lam;
       }
-      if (j < nv && q.active) {
-        *reinterpret_cast<Raw<BF16, V>*>(xb + j * dim * es + off) = Raw<BF16, V>::make(ox);
-        *reinterpret_cast<Raw<BF16, V>*>(gb + j * dim * es + off) = Raw<BF16, V>::make(og);
-        if (FORM == kGatedLru)
-          *reinterpret_cast<Raw<BF16, V>*>(ib + j * dim * es + off) = Raw<BF16, V>::make(oi);
-      }
-    }
-  }
-  if (a.dh0 != nullptr && q.chunk == 0 && q.active && q.row == 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) a.dh0[state_at + v] = mu[v];
-  }
+      for (int j = K - 1; j >= 0; --j) {
+        const bool rs = RESET && ((resets >> j) & 1u);
+#pragma unroll
+        for (int v = 0; v < V; ++v) m[v] = rs ? 0.f : da[j][v] * (m[v] + rd[j].get(v));
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        p[v] = RESET && resets != 0 ? 0.f : fmaxf(p[v], kTinyP);
+        pr[v] = p[v];
+      }
+      float pe[V], he[V], qe[V], me[V];
+      wave_scan<RESET, 1, V>(q.lane, a.cols, p, h, pe, he);
+      wave_scan<RESET, -1, V>(q.lane, a.cols, pr, m, qe, me);
+      if (q.lane >= 64 - a.cols) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) tot[q.wave][q.col * V + v] = make_float2(p[v], h[v]);
+      }
+      if (q.lane < a.cols) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) tom[q.wave][q.col * V + v] = m[v];
+      }
+      lds_sync();
+      if (q.wave == 0) {   // one channel a lane
+        const int64_t c = q.c0 - q.col * V + q.lane;
+        const bool on = q.lane < a.cols * V && c < dim;
+        const int64_t at = q.b * dim + (on ? c : 0);
+        float pt = 1.f, mt = 0.f;
+        for (int w = NW - 1; w >= 0; --w) {
+          float p2 = tot[w][on ? q.lane : 0].x, m2 = tom[w][on ? q.lane : 0];
+          then<RESET>(pt, mt, p2, m2);
+          pt = p2; mt = m2;
+        }
+        const int64_t slot = q.tile * plane + at, later = a.ntiles - 1 - q.tile;
+        if (on && a.ntiles > 1) publish(a.ws_maps + slot, word(__builtin_bit_cast(unsigned, pt), mt));
+        float min = 0.f;
+        if (later > 0) min = entering<RESET>(a.ws_maps, a.ws_ends, later, [&](int64_t k) { return slot + k * plane; }, on);
+        else if (on && a.dh_final != nullptr) min = a.dh_final[at];
+        const float mout = after<RESET>(pt, mt, min);
+        if (on) {
+          if (a.ntiles > 1) publish(a.ws_ends + slot, word(0, mout));
+          if (a.dh0 != nullptr && q.tile == 0) a.dh0[at] = mout;
+          enter[q.lane] = min;
+        }
+      }
+      // h_{t-1} of the tile's tokens, from the state that enters it
+      for (int w = 0; w < q.wave; ++w)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float2 f = tot[w][q.col * V + v];
+          st[v] = after<RESET>(f.x, f.y, st[v]);
+        }
+#pragma unroll
+      for (int v = 0; v < V; ++v) st[v] = after<RESET>(pe[v], he[v], st[v]);
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        const bool rs = RESET && ((resets >> j) & 1u);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float b = hp[j][v];
+          hp[j][v] = st[v];
+          st[v] = rs ? b : fmaf(da[j][v], st[v], b);
+        }
+      }
+      lds_sync();
+#pragma unroll
+      for (int v = 0; v < V; ++v) ms[v] = enter[q.col * V + v];
+      for (int w = NW - 1; w > q.wave; --w)
+#pragma unroll
+        for (int v = 0; v < V; ++v) ms[v] = after<RESET>(tot[w][q.col * V + v].x, tom[w][q.col * V + v], ms[v]);
+#pragma unroll
+      for (int v = 0; v < V; ++v) ms[v] = after<RESET>(qe[v], me[v], ms[v]);
+    }
+    Raw<BF16, V> ox[K], og[K], oi[K];
+#pragma unroll
+    for (int j = K - 1; j >= 0; --j) {
+      const bool rs = RESET && ((resets >> j) & 1u);
+      float dx[V], dg[V], di[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float x = rx[j].get(v), lam = ms[v] + rd[j].get(v);
+        float gg = g[j][v];
+        forget(gg);
+        float dec = gg;
+        if constexpr (FORM == kGatedLru) {
+          float mm;
+          lru_decay<FF>(A[v] * gg, mm, dec);
+          const float w = fmaf(mm, dec, mm);
+          const float inv = w == 0.f ? 0.f : __builtin_amdgcn_rsqf(w);   // 1 / s, and no share where s is 0
+          float s = w * inv;
+          if (RESET) s = rs ? 1.f : s;
+          const float u = gi[j][v] * x, ls = lam * s;
+          float dag = lam * dec * gg * fmaf(-u * dec, inv, hp[j][v]);
+          if (RESET) dag = rs ? 0.f : dag;
+          if (!FF) dag = j < nv ? dag : 0.f;
+          accA[v] += dag;
+          dg[v] = dag * A[v] * (1.f - gg);
+          dx[v] = ls * gi[j][v];
+          di[v] = ls * u * (1.f - gi[j][v]);
+        } else {
+          dx[v] = rs ? lam : lam * gi[j][v];
+          dg[v] = rs ? 0.f : dx[v] * gg * (hp[j][v] - x);
+          di[v] = 0.f;
+        }
+        if (!FF) dec = j < nv ? dec : 1.f;
+        ms[v] = rs ? 0.f : dec * lam;
+      }
+      ox[j] = Raw<BF16, V>::make(dx);
+      og[j] = Raw<BF16, V>::make(dg);
+      oi[j] = Raw<BF16, V>::make(di);
+    }
+    if (q.active) {
+      store_run<BF16, V, K, FF>(a.dx, first, step, off, nv, ox);
+      store_run<BF16, V, K, FF>(a.dr, first, step, off, nv, og);
+      if (FORM == kGatedLru) store_run<BF16, V, K, FF>(a.di, first, step, off, nv, oi);
+    }
+  };
+  if ((FORM != kGatedLru || __all(near1)) && q.t0 + T <= L) run(std::true_type{});
+  else run(std::false_type{});
+
   if (FORM == kGatedLru) {
     // rows of the wave, then the waves, in a fixed order
     for (int sh = a.cols; sh < 64; sh <<= 1)
@@ -579,26 +661,42 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_kernel(GatedArgs a) {
     __syncthreads();
     if (q.lane < a.cols) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) tom[0][q.wave][q.col][v] = accA[v];
+      for (int v = 0; v < V; ++v) tom[q.wave][q.col * V + v] = accA[v];
     }
     lds_sync();
     if (q.active && q.row == 0) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float s = 0.f;
-        for (int w = 0; w < kWaves; ++w) s += tom[0][w][q.col][v];
-        a.ws_da[q.chunk * plane + state_at + v] = s;
+        for (int w = 0; w < NW; ++w) s += tom[w][q.col * V + v];
+        a.ws_da[q.tile * plane + state_at + v] = s;
       }
     }
   }
 }
 
-// dA[d] = sum of the parts (chunk, batch) of channel d, in a fixed order.
-__global__ __launch_bounds__(256) void gated_da_kernel(const float* parts, float* dA, int64_t n, int64_t dim) {
-  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= dim) return;
+// Clears the published words and the counter of a pass.
+__global__ __launch_bounds__(256) void gated_clear_kernel(uint64_t* words, int64_t n, unsigned* count) {
+  const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
+  if (k == 0) *count = 0;
+  if (k < n) words[k] = ~0ull;
+  if (k + 1 < n) words[k + 1] = ~0ull;
+}
+
+// dA[d] = sum of the parts (tile, batch) of channel d, in a fixed order: 32
+// channels by 32 slices of the parts.
+__global__ __launch_bounds__(1024) void gated_da_kernel(const float* parts, float* dA, int64_t n, int64_t dim) {
+  __shared__ float red[32][33];
+  const int col = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + col;
   float s = 0.f;
-  for (int64_t k = 0; k < n; ++k) s += parts[k * dim + c];
+  if (c < dim)
+    for (int64_t k = slice; k < n; k += 32) s += parts[k * dim + c];
+  red[slice][col] = s;
+  lds_sync();
+  if (slice != 0 || c >= dim) return;
+  s = 0.f;
+  for (int k = 0; k < 32; ++k) s += red[k][col];
   dA[c] = s;
 }
 
@@ -617,48 +715,43 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedArgs a) {
   float st[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const Gate w = gate_of<FORM>(rr.get(v), FORM == kGatedLru ? a.A[c + v] : 0.f);
-    float u = rx.get(v);
-    if (FORM == kGatedLru) u *= sigmoid(ri.get(v));
-    st[v] = fmaf(w.a, a.states[k + v], w.s * u);
+    float dec, b;
+    gates<FORM, false, false>(rr.get(v), FORM == kGatedLru ? ri.get(v) : 0.f, rx.get(v), FORM == kGatedLru ? a.A[c + v] : 0.f,
+                              false, dec, b);
+    st[v] = fmaf(dec, a.states[k + v], b);
     a.states[k + v] = st[v];
   }
   *reinterpret_cast<R*>((char*)a.y + k * es) = R::make(st);
 }
 
-constexpr int run_len(bool bf16) { return bf16 ? 16 : 8; }   // tokens of a lane's run
+constexpr int run_len(bool bf16) { return bf16 ? KF : 8; }   // tokens of a lane's run, forward
+constexpr int kRunBwd = KB;
 
-template <bool BF16, int V, int FORM, bool RESET>
-void launch_fwd(const GatedArgs& a, unsigned grid, hipStream_t st) {
-  constexpr int K = run_len(BF16);
-  if (a.nchunks > 1) gated_fwd_kernel<BF16, V, FORM, RESET, K, true><<<grid, kThreads, 0, st>>>(a);
-  gated_fwd_kernel<BF16, V, FORM, RESET, K, false><<<grid, kThreads, 0, st>>>(a);
-}
-
-template <bool BF16, int V, int FORM, bool RESET>
-void launch_bwd(const GatedArgs& a, unsigned grid, hipStream_t st) {
-  constexpr int K = 8;
-  if (a.nchunks > 1) gated_bwd_agg_kernel<BF16, V, FORM, RESET, K><<<grid, kThreads, 0, st>>>(a);
-  gated_bwd_kernel<BF16, V, FORM, RESET, K><<<grid, kThreads, 0, st>>>(a);
+template <bool BF16, int V, int FORM, bool RESET, int NW>
+void launch(const GatedArgs& a, unsigned grid, bool bwd, hipStream_t st) {
+  if (bwd) gated_bwd_kernel<BF16, V, FORM, RESET, kRunBwd, NW><<<grid, 64 * NW, 0, st>>>(a);
+  else gated_fwd_kernel<BF16, V, FORM, RESET, run_len(BF16), NW><<<grid, 64 * NW, 0, st>>>(a);
 }
 
 // Instances: V = 2 where the rows allow it, with and without resets; the
 // one-channel kernels always look for them.
-template <bool BF16, int FORM>
-void pick(const GatedArgs& a, unsigned grid, bool bwd, hipStream_t st) {
-  if (a.vec) {
-    if (a.reset != nullptr) bwd ? launch_bwd<BF16, 2, FORM, true>(a, grid, st) : launch_fwd<BF16, 2, FORM, true>(a, grid, st);
-    else bwd ? launch_bwd<BF16, 2, FORM, false>(a, grid, st) : launch_fwd<BF16, 2, FORM, false>(a, grid, st);
-  } else {
-    bwd ? launch_bwd<BF16, 1, FORM, true>(a, grid, st) : launch_fwd<BF16, 1, FORM, true>(a, grid, st);
-  }
+template <bool BF16, int V, int FORM, bool RESET>
+void pick(const GatedArgs& a, unsigned grid, int waves, bool bwd, hipStream_t st) {
+  if (waves == 4) launch<BF16, V, FORM, RESET, 4>(a, grid, bwd, st);
+  else if (waves == 8) launch<BF16, V, FORM, RESET, 8>(a, grid, bwd, st);
+  else launch<BF16, V, FORM, RESET, 16>(a, grid, bwd, st);
 }
-
-void pick(const GatedArgs& a, unsigned grid, bool bwd, hipStream_t st) {
+template <bool BF16, int FORM>
+void pick(const GatedArgs& a, unsigned grid, int waves, bool bwd, hipStream_t st) {
+  if (!a.vec) pick<BF16, 1, FORM, true>(a, grid, waves, bwd, st);
+  else if (a.reset != nullptr) pick<BF16, 2, FORM, true>(a, grid, waves, bwd, st);
+  else pick<BF16, 2, FORM, false>(a, grid, waves, bwd, st);
+}
+void pick(const GatedArgs& a, unsigned grid, int waves, bool bwd, hipStream_t st) {
   if (a.act_bf16) {
-    a.form == kGatedLru ? pick<true, kGatedLru>(a, grid, bwd, st) : pick<true, kGatedUnit>(a, grid, bwd, st);
+    a.form == kGatedLru ? pick<true, kGatedLru>(a, grid, waves, bwd, st) : pick<true, kGatedUnit>(a, grid, waves, bwd, st);
   } else {
-    a.form == kGatedLru ? pick<false, kGatedLru>(a, grid, bwd, st) : pick<false, kGatedUnit>(a, grid, bwd, st);
+    a.form == kGatedLru ? pick<false, kGatedLru>(a, grid, waves, bwd, st) : pick<false, kGatedUnit>(a, grid, waves, bwd, st);
   }
 }
 
@@ -666,82 +759,70 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-GatedPlan plan_gated(int64_t batch, int64_t seqlen, int64_t dim, bool bf16, int num_cus) {
-  GatedPlan p{kGatedMaxCols, 1, 1, 0, 0, 0};
+// Columns: as many lanes across the channels as there are channels for, up to 32 (a 128-byte row of bf16
+// pairs); the other lanes go along time.
+GatedPlan plan_gated(int64_t batch, int64_t seqlen, int64_t dim, bool bf16, bool bwd) {
+  GatedPlan p{4, 8, 0, 1, 0, 0, 0};
   if (batch == 0 || dim == 0) return p;
   const int V = dim % 2 == 0 ? 2 : 1;
-  auto groups = [&](int cols) { return batch * ((dim + (int64_t)cols * V - 1) / ((int64_t)cols * V)); };
-  while (p.cols > 4 && groups(p.cols) < 2 * num_cus) p.cols /= 2;
-  // the forward and the backward share the plan, so a chunk is whole tiles of both
-  const int64_t T = (int64_t)kWaves * (64 / p.cols) * std::max(run_len(bf16), 8);
-  const int64_t tiles = (seqlen + T - 1) / T;
-  if (groups(p.cols) < num_cus && tiles > 1) {
-    p.nchunks = std::min<int64_t>(std::min<int64_t>((num_cus + groups(p.cols) - 1) / groups(p.cols), tiles), 64);
-  }
-  const int64_t per = std::max<int64_t>(1, (tiles + p.nchunks - 1) / p.nchunks);
-  p.chunk_len = per * T;
-  p.nchunks = std::max<int64_t>(1, (tiles + per - 1) / per);
-  const size_t plane = (size_t)(batch * dim) * sizeof(float);
-  p.maps_bytes = p.nchunks > 1 ? up256(plane) + 2 * up256(p.nchunks * plane) : 0;
-  p.da_bytes = up256(p.nchunks * plane);
-  p.states_bytes = (size_t)((seqlen + kGatedSave - 1) / kGatedSave) * plane;
+  while (p.cols < kGatedMaxCols && (int64_t)p.cols * V < dim) p.cols *= 2;
+  if (const char* e = getenv("GW")) p.waves = atoi(e);
+  if (const char* e = getenv("GC")) p.cols = atoi(e);
+  p.tile = (int64_t)p.waves * (64 / p.cols) * (bwd ? kRunBwd : run_len(bf16));
+  p.ntiles = std::max<int64_t>(1, (seqlen + p.tile - 1) / p.tile);
+  const size_t plane = (size_t)(batch * dim);
+  p.words_bytes = p.ntiles > 1 ? up256(2 * p.ntiles * plane * sizeof(uint64_t)) + 256 : 0;
+  p.da_bytes = bwd ? up256(p.ntiles * plane * sizeof(float)) : 0;
+  p.states_bytes = (size_t)((seqlen + kGatedSave - 1) / kGatedSave) * plane * sizeof(float);
   return p;
 }
 
-static void set_maps(GatedArgs& a, const GatedPlan& p, char* ws) {
-  const size_t plane = up256((size_t)(a.batch * a.dim) * sizeof(float));
-  const size_t planes = up256((size_t)p.nchunks * (size_t)(a.batch * a.dim) * sizeof(float));
-  a.ws_h0 = (float*)ws;
-  a.ws_p = (float*)(ws + plane);
-  a.ws_h = (float*)(ws + plane + planes);
-}
-
-static int grid_of(const GatedArgs& a, const GatedPlan& p, unsigned* grid) {
+// One pass with its plan: clears the published words, then the kernel.
+static int run_pass(GatedArgs a, const GatedPlan& p, bool bwd, void* ws, hipStream_t st) {
   const int V = a.vec ? 2 : 1;
   const int64_t cw = (int64_t)p.cols * V;
-  const int64_t n = ((a.dim + cw - 1) / cw) * a.batch * p.nchunks;
+  const int64_t n = ((a.dim + cw - 1) / cw) * a.batch * p.ntiles;
   // a lane's byte offset in a tile is held in 32 bits
-  const int64_t tile = (int64_t)kWaves * (64 / p.cols) * 16 * (a.act_bf16 ? 2 : 4);
-  if (n > 0x7fffffffLL || a.dim > 0x7fffffffLL / tile) return fail(4, "batch or dim too large");
-  *grid = (unsigned)n;
-  return 0;
-}
-
-int launch_gated_fwd(GatedArgs a, const GatedPlan& p, void* ws, void* stream) {
-  unsigned grid = 0;
-  const int rc = grid_of(a, p, &grid);
-  if (rc != 0) return rc;
-  a.cols = p.cols; a.nchunks = p.nchunks; a.chunk_len = p.chunk_len;
-  if (p.nchunks > 1) set_maps(a, p, (char*)ws);
-  pick(a, grid, false, (hipStream_t)stream);
+  if (n > 0x7fffffffLL || a.dim > 0x7fffffffLL / (p.tile * (a.act_bf16 ? 2 : 4))) return fail(4, "batch, seqlen or dim too large");
+  a.cols = p.cols; a.ntiles = p.ntiles;
+  if (p.ntiles > 1) {
+    const int64_t words = 2 * p.ntiles * a.batch * a.dim, blocks = (words + 511) / 512;
+    if (blocks > 0x7fffffffLL) return fail(4, "batch, seqlen or dim too large");
+    a.ws_count = (unsigned*)ws;
+    a.ws_maps = (uint64_t*)((char*)ws + 256);
+    a.ws_ends = a.ws_maps + words / 2;
+    gated_clear_kernel<<<(unsigned)blocks, 256, 0, st>>>(a.ws_maps, words, a.ws_count);
+  }
+  pick(a, (unsigned)n, p.waves, bwd, st);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? 0 : fail(6, std::string("gated scan launch: ") + hipGetErrorString(e));
 }
 
-// Workspace: the chunk maps, the dA parts and, without the forward's states, the states.
-int launch_gated_bwd(GatedArgs a, const GatedPlan& p, void* ws, void* stream) {
-  unsigned grid = 0;
-  const int rc = grid_of(a, p, &grid);
-  if (rc != 0) return rc;
+int launch_gated_fwd(GatedArgs a, const GatedPlan& p, void* ws, void* stream) {
+  return run_pass(a, p, false, ws, (hipStream_t)stream);
+}
+
+// Workspace: the published words (of the two passes, one after the other), the dA parts and, without the
+// forward's states, the states.
+int launch_gated_bwd(GatedArgs a, const GatedPlan& fwd, const GatedPlan& p, void* ws, void* stream) {
   hipStream_t st = (hipStream_t)stream;
-  if (a.batch == 0) {   // dA of no rows
-    if (a.form == kGatedLru) gated_da_kernel<<<(unsigned)((a.dim + 255) / 256), 256, 0, st>>>(nullptr, a.dA, 0, a.dim);
-    const hipError_t e0 = hipGetLastError();
-    return e0 == hipSuccess ? 0 : fail(6, std::string("gated scan backward launch: ") + hipGetErrorString(e0));
+  int rc = 0;
+  char* const parts = (char*)ws + std::max(p.words_bytes, a.saved == nullptr ? fwd.words_bytes : 0);
+  if (a.batch > 0) {
+    a.ws_da = (float*)parts;
+    if (a.saved == nullptr) {
+      a.states = (float*)(parts + p.da_bytes);
+      rc = run_pass(a, fwd, false, ws, st);   // y and h_final are null: the states only
+      a.saved = a.states;
+    }
+    if (rc == 0) rc = run_pass(a, p, true, ws, st);
   }
-  a.cols = p.cols; a.nchunks = p.nchunks; a.chunk_len = p.chunk_len;
-  if (p.nchunks > 1) set_maps(a, p, (char*)ws);
-  a.ws_da = (float*)((char*)ws + p.maps_bytes);
-  if (a.saved == nullptr) {
-    a.states = (float*)((char*)ws + p.maps_bytes + p.da_bytes);
-    pick(a, grid, false, st);   // y and h_final are null: the states only
-    a.saved = a.states;
+  if (rc == 0 && a.form == kGatedLru) {
+    gated_da_kernel<<<(unsigned)((a.dim + 31) / 32), 1024, 0, st>>>((const float*)parts, a.dA, p.ntiles * a.batch, a.dim);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(6, std::string("gated scan backward launch: ") + hipGetErrorString(e));
   }
-  pick(a, grid, true, st);
-  if (a.form == kGatedLru)
-    gated_da_kernel<<<(unsigned)((a.dim + 255) / 256), 256, 0, st>>>(a.ws_da, a.dA, p.nchunks * a.batch, a.dim);
-  const hipError_t e = hipGetLastError();
-  return e == hipSuccess ? 0 : fail(6, std::string("gated scan backward launch: ") + hipGetErrorString(e));
+  return rc;
 }
 
 int launch_gated_step(const GatedArgs& a, void* stream) {

@@ -258,12 +258,12 @@ struct GatedArgs {
   float* dA;
   float* dh0;
   // workspace
-  float* ws_h0;                // (batch, dim): state entering the first chunk
-  float* ws_p;                 // (nchunks, batch, dim): maps of the time chunks
-  float* ws_h;
-  float* ws_da;                // (nchunks, batch, dim)
+  unsigned* ws_count;          // tiles taken
+  uint64_t* ws_maps;           // (ntiles, batch, dim): the tiles' maps, and the states after them
+  uint64_t* ws_ends;
+  float* ws_da;                // (ntiles, batch, dim)
   int64_t batch, seqlen, dim;
-  int64_t nchunks, chunk_len;
+  int64_t ntiles;
   int cols;                    // lanes across channels: 4, 8, 16 or 32
   int form;
   int act_bf16;
@@ -271,14 +271,19 @@ struct GatedArgs {
 };
 
 struct GatedPlan {
-  int cols;
-  int64_t nchunks, chunk_len;
-  size_t maps_bytes, da_bytes, states_bytes;
+  int cols, waves;             // lanes across channels; waves of a workgroup
+  int64_t tile, ntiles;        // tokens of a tile
+  size_t words_bytes, da_bytes, states_bytes;
 };
-GatedPlan plan_gated(int64_t batch, int64_t seqlen, int64_t dim, bool bf16, int num_cus);
-// ws: maps_bytes (forward); maps_bytes + da_bytes, and states_bytes where a.saved is null (backward)
+GatedPlan plan_gated(int64_t batch, int64_t seqlen, int64_t dim, bool bf16, bool bwd);
+// ws: words_bytes of the plan
 int launch_gated_fwd(GatedArgs a, const GatedPlan& p, void* ws, void* stream);
-int launch_gated_bwd(GatedArgs a, const GatedPlan& p, void* ws, void* stream);
+// ws: gated_bwd_ws_bytes; fwd: the forward's plan, for the states where a.saved is null
+inline size_t gated_bwd_ws_bytes(const GatedPlan& fwd, const GatedPlan& bwd, bool have_states) {
+  const size_t words = have_states || bwd.words_bytes > fwd.words_bytes ? bwd.words_bytes : fwd.words_bytes;
+  return words + bwd.da_bytes + (have_states ? 0 : bwd.states_bytes);
+}
+int launch_gated_bwd(GatedArgs a, const GatedPlan& fwd, const GatedPlan& bwd, void* ws, void* stream);
 int launch_gated_step(const GatedArgs& a, void* stream);
 
 // ---------------------------------------------------------------- block norm
