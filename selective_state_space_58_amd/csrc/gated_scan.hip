@@ -29,27 +29,7 @@
 namespace ssm {
 namespace {
 
-#ifndef UW
-#define UW 1
-#endif
-#ifndef KF
-#define KF 16
-#endif
-#ifndef KB
-#define KB 8
-#endif
-#ifndef PF
-#define PF 1
-#endif
-#ifndef PB
-#define PB 1
-#endif
-#ifndef WF
-#define WF 1
-#endif
-#ifndef WB
-#define WB 1
-#endif
+constexpr int NW = 8;   // waves of a workgroup
 constexpr float kLog2e = 1.4426950408889634f;
 // Products of decays are kept from underflowing, so that P == 0 says that the
 // run holds a reset, after which nothing of before (not even a NaN) is left.
@@ -65,9 +45,7 @@ struct Raw<true, 2> {
     return __builtin_bit_cast(float, v == 0 ? u << 16 : u & 0xffff0000u);
   }
   static __device__ __forceinline__ Raw make(const float (&f)[2]) {
-    const unsigned lo = __builtin_bit_cast(unsigned short, (__bf16)f[0]);
-    const unsigned hi = __builtin_bit_cast(unsigned short, (__bf16)f[1]);
-    return {lo | (hi << 16)};
+    return {pack_bf16(f[0], f[1])};
   }
 };
 template <>
@@ -206,85 +184,91 @@ __device__ __forceinline__ float low(uint64_t w) { return __builtin_bit_cast(flo
 __device__ __forceinline__ unsigned high(uint64_t w) { return (unsigned)(w >> 32); }
 
 // The state that enters a tile from the `before` tiles before it in the order
-// of the scan, for one channel a lane, called by one whole wave.  at(k) is the
-// place of the k-th tile before (k from 1).  The state is always folded tile
-// after tile from a known end state, which itself was folded so: the same
-// bits, whatever tile the fold starts from.  It waits only for maps, which
-// every tile publishes before it waits for anything, and for the first tile's
-// end state, which waits for nothing.
-constexpr int kAhead = 8;   // words read at a time
+// of the scan.  The waves look at kWindow tiles at a time, a channel a lane,
+// nearest first: at the tiles' ends, and at their maps, which they keep in LDS
+// until a known end is found, at most kHist tiles back.  One wave then folds
+// the maps onto it.  The state is always folded tile after tile from a known
+// end, which itself was folded so: the same bits, whatever tile the fold starts
+// from.  Every wait ends: a tile publishes its map before it waits, the first
+// tile's end waits for nothing, and the first of the tiles whose ends are still
+// missing finds the end of the tile next to it.
+constexpr int kWindow = 8, kHist = 64;
+struct Looked {
+  uint64_t maps[kHist][kGatedMaxCols * 2];
+  float ends[kWindow][kGatedMaxCols * 2];
+  int known[kWindow];   // bit 0: the end, bit 1: the map
+};
 template <bool RESET, class At>
-__device__ __forceinline__ float entering(const uint64_t* maps, const uint64_t* ends, int64_t before, At at, bool on) {
-  // the nearest tile with a known end state
-  int64_t k = 1;
-  uint64_t w[kAhead];
-  float h = 0.f;
-  for (bool found = false; !found;) {
+__device__ __forceinline__ float entering(Looked& s, const uint64_t* maps, const uint64_t* ends, int64_t before, At at,
+                                          bool on, int wave, int lane) {
+  int base = 1;   // distance of the window's nearest tile
+  for (;;) {
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) w[j] = on && k + j <= before ? look(ends + at(k + j)) : 0;
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (!found && k + j <= before && __all(high(w[j]) == 0)) {
-        found = true;
-        h = low(w[j]);
-        k += j;
-        break;
+    for (int p = 0; p < kWindow / NW; ++p) {
+      const int j = wave + p * NW, d = base + j;
+      const bool in = d <= before;
+      const uint64_t e = on && in ? look(ends + at(d)) : 0, m = on && in ? look(maps + at(d)) : 0;
+      s.maps[d - 1][lane] = m;
+      s.ends[j][lane] = low(e);
+      const bool end = __all(high(e) == 0), map = __all(high(m) != kUnset);
+      if (lane == 0) s.known[j] = in ? (end ? 1 : 0) | (map ? 2 : 0) : 0;
+    }
+    lds_sync();
+    const int k = lane < kWindow ? s.known[lane] : 0;
+    const unsigned have_end = (unsigned)__ballot((k & 1) != 0), have_map = (unsigned)__ballot((k & 2) != 0);
+    const int f = __builtin_ctz(have_end | (1u << kWindow));   // the nearest known end, kWindow if none
+    if ((~have_map & ((1u << f) - 1)) == 0) {                  // with the maps of the tiles between
+      if (f < kWindow) {
+        float h = 0.f;
+        if (wave == 0) {
+          h = s.ends[f][lane];
+          for (int d = base + f - 1; d > 0; --d) {
+            const uint64_t m = s.maps[d - 1][lane];
+            h = after<RESET>(__builtin_bit_cast(float, high(m)), low(m), h);
+          }
+        }
+        return h;
       }
+      // further back, while there are tiles there (the first tile's map is out before its end)
+      if (base + kWindow <= before && base + 2 * kWindow - 1 <= kHist) base += kWindow;
     }
-    if (!found) {
-      k = k + kAhead <= before ? k + kAhead : before;   // in the end the first tile's, which is waited for
-      if (k == before) __builtin_amdgcn_s_sleep(1);
-    }
+    __builtin_amdgcn_s_sleep(1);
+    lds_sync();   // the words are read before they are looked at again
   }
-  // the maps from there to this tile
-  for (--k; k > 0;) {
-    const int n = k < kAhead ? (int)k : kAhead;
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) w[j] = on && j < n ? look(maps + at(k - j)) : 0;
-    int done = 0;
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (j < n && done == j && __all(high(w[j]) != kUnset)) {
-        h = after<RESET>(__builtin_bit_cast(float, high(w[j])), low(w[j]), h);
-        done = j + 1;
-      }
-    }
-    k -= done;
-    if (done == 0) __builtin_amdgcn_s_sleep(1);
-  }
-  return h;
 }
 
-// K tokens of one lane, from element `first` on: the tile's address in scalar
-// registers, the lane's byte offset in a vector register, the token's in a
-// scalar one (a buffer access; with plain addresses the compiler adds the token
-// to the lane's offset, a vector instruction for each).  The tokens from nv on
-// are left alone.  FULL: nv is K.
-constexpr int kBufferFlags = 0x00027000;   // raw 32-bit elements
-template <bool BF16, int V, int K, bool FULL>
-__device__ __forceinline__ void load_run(const void* src, int64_t first, unsigned step, unsigned off, int nv,
-                                         Raw<BF16, V> (&out)[K]) {
-  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((char*)src + first * (BF16 ? 2 : 4), 0, 0x7fffffff, kBufferFlags);
-#pragma unroll
-  for (int j = 0; j < K; ++j) {
-    if (!FULL && j >= nv) continue;
-    if constexpr (sizeof(out[j]) == 2) out[j] = __builtin_bit_cast(Raw<BF16, V>, __builtin_amdgcn_raw_buffer_load_b16(rsrc, off, j * step, 0));
-    else if constexpr (sizeof(out[j]) == 4) out[j] = __builtin_bit_cast(Raw<BF16, V>, __builtin_amdgcn_raw_buffer_load_b32(rsrc, off, j * step, 0));
-    else out[j] = __builtin_bit_cast(Raw<BF16, V>, __builtin_amdgcn_raw_buffer_load_b64(rsrc, off, j * step, 0));
+// The rows of one tensor in a tile: the tile's address in scalar registers, the
+// lane's byte offset in a vector register, the token's in a scalar one (a buffer
+// access; with plain addresses the compiler adds the token to the lane's offset,
+// a vector instruction for each).
+template <bool BF16, int V>
+struct Rows {
+  using R = Raw<BF16, V>;
+  __amdgpu_buffer_rsrc_t rsrc;
+  unsigned off, step;
+  __device__ __forceinline__ Rows(const void* p, int64_t first, unsigned off, unsigned step)
+      : rsrc(__builtin_amdgcn_make_buffer_rsrc((char*)p + first * (BF16 ? 2 : 4), 0, 0x7fffffff, 0x00027000)),
+        off(off), step(step) {}
+  __device__ __forceinline__ R load(int j) const {
+    if constexpr (sizeof(R) == 2) return __builtin_bit_cast(R, __builtin_amdgcn_raw_buffer_load_b16(rsrc, off, j * step, 0));
+    else if constexpr (sizeof(R) == 4) return __builtin_bit_cast(R, __builtin_amdgcn_raw_buffer_load_b32(rsrc, off, j * step, 0));
+    else return __builtin_bit_cast(R, __builtin_amdgcn_raw_buffer_load_b64(rsrc, off, j * step, 0));
   }
-}
-template <bool BF16, int V, int K, bool FULL>
-__device__ __forceinline__ void store_run(void* dst, int64_t first, unsigned step, unsigned off, int nv,
-                                          const Raw<BF16, V> (&v)[K]) {
-  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((char*)dst + first * (BF16 ? 2 : 4), 0, 0x7fffffff, kBufferFlags);
-#pragma unroll
-  for (int j = 0; j < K; ++j) {
-    if (!FULL && j >= nv) continue;
-    if constexpr (sizeof(v[j]) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v[j]), rsrc, off, j * step, 0);
-    else if constexpr (sizeof(v[j]) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v[j]), rsrc, off, j * step, 0);
-    else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v[j]), rsrc, off, j * step, 0);
+  __device__ __forceinline__ void store(int j, R v) const {
+    if constexpr (sizeof(R) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), rsrc, off, j * step, 0);
+    else if constexpr (sizeof(R) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), rsrc, off, j * step, 0);
+    else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), rsrc, off, j * step, 0);
   }
-}
+  // K tokens; without FULL those from nv on are zeros
+  template <bool FULL, int K>
+  __device__ __forceinline__ void load(R (&out)[K], int nv) const {
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      if (!FULL) out[j] = {};
+      if (FULL || j < nv) out[j] = load(j);
+    }
+  }
+};
 
 // Reset flags of a lane's run as a bit mask.
 template <int K>
@@ -327,10 +311,11 @@ __device__ __forceinline__ void wave_scan(int lane, int cols, float (&p)[V], flo
 }
 
 // Forward: y, the states entering every kGatedSave-th token and the final state.
-template <bool BF16, int V, int FORM, bool RESET, int K, int NW>
-__global__ __launch_bounds__(64 * NW) void gated_fwd_kernel(GatedArgs a) {
+template <bool BF16, int V, int FORM, bool RESET, int K>
+__global__ __launch_bounds__(64 * NW, 4) void gated_fwd_kernel(GatedArgs a) {
   __shared__ float2 tot[NW][kGatedMaxCols * V];
   __shared__ float enter[kGatedMaxCols * V];
+  __shared__ Looked looked;
   const int T = NW * (64 / a.cols) * K;
   const Place q = place<V, 1>(a, T);
   const int64_t L = a.seqlen, dim = a.dim;
@@ -357,12 +342,9 @@ __global__ __launch_bounds__(64 * NW) void gated_fwd_kernel(GatedArgs a) {
     unsigned resets = 0;
     {
       Raw<BF16, V> rr[K], ri[K], rx[K];
-      if (!FF)
-#pragma unroll
-        for (int j = 0; j < K; ++j) { rr[j] = {}; ri[j] = {}; rx[j] = {}; }
-      load_run<BF16, V, K, FF>(a.r, first, step, off, nv, rr);
-      if (FORM == kGatedLru) load_run<BF16, V, K, FF>(a.i, first, step, off, nv, ri);
-      load_run<BF16, V, K, FF>(a.x, first, step, off, nv, rx);
+      Rows<BF16, V>(a.r, first, off, step).template load<FF>(rr, nv);
+      if (FORM == kGatedLru) Rows<BF16, V>(a.i, first, off, step).template load<FF>(ri, nv);
+      Rows<BF16, V>(a.x, first, off, step).template load<FF>(rx, nv);
       if (RESET) resets = load_resets<K>(a.reset, q.b * L + tl, nv);
 #pragma unroll
       for (int v = 0; v < V; ++v) { p[v] = 1.f; h[v] = 0.f; }
@@ -391,24 +373,27 @@ __global__ __launch_bounds__(64 * NW) void gated_fwd_kernel(GatedArgs a) {
       for (int v = 0; v < V; ++v) tot[q.wave][q.col * V + v] = make_float2(p[v], h[v]);
     }
     lds_sync();
-    if (q.wave == 0) {   // one channel a lane
+    {   // one channel a lane
       const int64_t c = q.c0 - q.col * V + q.lane;
       const bool on = q.lane < a.cols * V && c < dim;
-      const int64_t at = q.b * dim + (on ? c : 0);
-      float pt = 1.f, ht = 0.f;
-      for (int w = 0; w < NW; ++w) {
-        const float2 f = tot[w][on ? q.lane : 0];
-        float p2 = f.x, h2 = f.y;
-        then<RESET>(pt, ht, p2, h2);
-        pt = p2; ht = h2;
+      const int64_t at = q.b * dim + (on ? c : 0), slot = q.tile * plane + at;
+      float pt = 1.f, ht = 0.f, hin = 0.f;
+      if (q.wave == 0) {
+#pragma unroll 4
+        for (int w = 0; w < NW; ++w) {
+          const float2 f = tot[w][on ? q.lane : 0];
+          float p2 = f.x, h2 = f.y;
+          then<RESET>(pt, ht, p2, h2);
+          pt = p2; ht = h2;
+        }
+        if (on && a.ntiles > 1) publish(a.ws_maps + slot, word(__builtin_bit_cast(unsigned, pt), ht));
+        if (on && q.tile == 0 && a.h0 != nullptr) hin = a.h0[at];
       }
-      const int64_t slot = q.tile * plane + at;
-      if (on && a.ntiles > 1) publish(a.ws_maps + slot, word(__builtin_bit_cast(unsigned, pt), ht));
-      float hin = 0.f;
-      if (q.tile > 0) hin = entering<RESET>(a.ws_maps, a.ws_ends, q.tile, [&](int64_t k) { return slot - k * plane; }, on);
-      else if (on && a.h0 != nullptr) hin = a.h0[at];
-      const float hout = after<RESET>(pt, ht, hin);
-      if (on) {
+      if (q.tile > 0)
+        hin = entering<RESET>(looked, a.ws_maps, a.ws_ends, q.tile, [&](int64_t k) { return slot - k * plane; }, on,
+                                  q.wave, q.lane);
+      if (q.wave == 0 && on) {
+        const float hout = after<RESET>(pt, ht, hin);
         if (a.ntiles > 1) publish(a.ws_ends + slot, word(0, hout));
         if (a.h_final != nullptr && q.tile == a.ntiles - 1) a.h_final[at] = hout;
         enter[q.lane] = hin;
@@ -418,6 +403,7 @@ __global__ __launch_bounds__(64 * NW) void gated_fwd_kernel(GatedArgs a) {
     float st[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) st[v] = enter[q.col * V + v];
+#pragma unroll 1
     for (int w = 0; w < q.wave; ++w)
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -431,15 +417,15 @@ __global__ __launch_bounds__(64 * NW) void gated_fwd_kernel(GatedArgs a) {
       for (int v = 0; v < V; ++v) a.states[(tl / kGatedSave) * plane + state_at + v] = st[v];
     }
     if (a.y == nullptr) return;
-    Raw<BF16, V> out[K];
+    const Rows<BF16, V> y(a.y, first, off, step);
+    if (!q.active) return;
 #pragma unroll
     for (int j = 0; j < K; ++j) {
       const bool rs = RESET && ((resets >> j) & 1u);
 #pragma unroll
       for (int v = 0; v < V; ++v) st[v] = rs ? db[j][v] : fmaf(da[j][v], st[v], db[j][v]);
-      out[j] = Raw<BF16, V>::make(st);
+      if (FF || j < nv) y.store(j, Raw<BF16, V>::make(st));
     }
-    if (q.active) store_run<BF16, V, K, FF>(a.y, first, step, off, nv, out);
   };
   if ((FORM != kGatedLru || __all(near1)) && q.t0 + T <= L) run(std::true_type{});
   else run(std::false_type{});
@@ -447,16 +433,21 @@ __global__ __launch_bounds__(64 * NW) void gated_fwd_kernel(GatedArgs a) {
 
 // Hides where a value comes from, so that what is formed from it again is
 // formed again and not kept in registers from the first time.
-__device__ __forceinline__ void forget(float& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void forget(float& v) { asm("" : "+v"(v)); }
+template <int V>
+__device__ __forceinline__ void forget(Raw<true, V>& r) { asm("" : "+v"(r.u)); }
+template <int V>
+__device__ __forceinline__ void forget(Raw<false, V>&) {}   // fp32 lies in memory as it is used
 
 // Backward: dx, dr, di, dh0 and the tile's share of dA.  The sigmoids are formed
 // once and kept; decay and root are formed from them for the scans, and again
 // for the gradients (13 instructions) instead of waiting in registers.
-template <bool BF16, int V, int FORM, bool RESET, int K, int NW>
-__global__ __launch_bounds__(64 * NW) void gated_bwd_kernel(GatedArgs a) {
+template <bool BF16, int V, int FORM, bool RESET, int K>
+__global__ __launch_bounds__(64 * NW, 4) void gated_bwd_kernel(GatedArgs a) {
   __shared__ float2 tot[NW][kGatedMaxCols * V];   // (P, H) of the waves' runs
   __shared__ float tom[NW][kGatedMaxCols * V];    // M of the waves' runs
   __shared__ float enter[kGatedMaxCols * V];
+  __shared__ Looked looked;
   const int T = NW * (64 / a.cols) * K;
   const Place q = place<V, -1>(a, T);
   const int64_t L = a.seqlen, dim = a.dim;
@@ -484,13 +475,10 @@ __global__ __launch_bounds__(64 * NW) void gated_bwd_kernel(GatedArgs a) {
     unsigned resets = 0;
     {
       Raw<BF16, V> rr[K], ri[K];
-      if (!FF)
-#pragma unroll
-        for (int j = 0; j < K; ++j) { rr[j] = {}; ri[j] = {}; rx[j] = {}; rd[j] = {}; }
-      load_run<BF16, V, K, FF>(a.r, first, step, off, nv, rr);
-      if (FORM == kGatedLru) load_run<BF16, V, K, FF>(a.i, first, step, off, nv, ri);
-      load_run<BF16, V, K, FF>(a.x, first, step, off, nv, rx);
-      load_run<BF16, V, K, FF>(a.dout, first, step, off, nv, rd);
+      Rows<BF16, V>(a.r, first, off, step).template load<FF>(rr, nv);
+      if (FORM == kGatedLru) Rows<BF16, V>(a.i, first, off, step).template load<FF>(ri, nv);
+      Rows<BF16, V>(a.x, first, off, step).template load<FF>(rx, nv);
+      Rows<BF16, V>(a.dout, first, off, step).template load<FF>(rd, nv);
       if (RESET) resets = load_resets<K>(a.reset, q.b * L + tl, nv);
 #pragma unroll
       for (int v = 0; v < V; ++v) st[v] = L > 0 ? a.saved[(q.t0 / kGatedSave) * plane + q.b * dim + c_ld + v] : 0.f;
@@ -556,30 +544,24 @@ __global__ __launch_bounds__(64 * NW) void gated_bwd_kernel(GatedArgs a) {
         for (int v = 0; v < V; ++v) tom[q.wave][q.col * V + v] = m[v];
       }
       lds_sync();
-      if (q.wave == 0) {   // one channel a lane
-        const int64_t c = q.c0 - q.col * V + q.lane;
-        const bool on = q.lane < a.cols * V && c < dim;
-        const int64_t at = q.b * dim + (on ? c : 0);
-        float pt = 1.f, mt = 0.f;
+      // one channel a lane
+      const int64_t c = q.c0 - q.col * V + q.lane;
+      const bool on = q.lane < a.cols * V && c < dim;
+      const int64_t at = q.b * dim + (on ? c : 0), slot = q.tile * plane + at, later = a.ntiles - 1 - q.tile;
+      float pt = 1.f, mt = 0.f, min = 0.f;
+      if (q.wave == 0) {
+#pragma unroll 4
         for (int w = NW - 1; w >= 0; --w) {
           float p2 = tot[w][on ? q.lane : 0].x, m2 = tom[w][on ? q.lane : 0];
           then<RESET>(pt, mt, p2, m2);
           pt = p2; mt = m2;
         }
-        const int64_t slot = q.tile * plane + at, later = a.ntiles - 1 - q.tile;
         if (on && a.ntiles > 1) publish(a.ws_maps + slot, word(__builtin_bit_cast(unsigned, pt), mt));
-        float min = 0.f;
-        if (later > 0) min = entering<RESET>(a.ws_maps, a.ws_ends, later, [&](int64_t k) { return slot + k * plane; }, on);
-        else if (on && a.dh_final != nullptr) min = a.dh_final[at];
-        const float mout = after<RESET>(pt, mt, min);
-        if (on) {
-          if (a.ntiles > 1) publish(a.ws_ends + slot, word(0, mout));
-          if (a.dh0 != nullptr && q.tile == 0) a.dh0[at] = mout;
-          enter[q.lane] = min;
-        }
+        if (on && later == 0 && a.dh_final != nullptr) min = a.dh_final[at];
       }
-      // h_{t-1} of the tile's tokens, from the state that enters it
-      for (int w = 0; w < q.wave; ++w)
+      // h_{t-1} of the tile's tokens, from the state that enters it (while the other tiles' maps come out)
+  #pragma unroll 1
+    for (int w = 0; w < q.wave; ++w)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const float2 f = tot[w][q.col * V + v];
@@ -597,20 +579,34 @@ __global__ __launch_bounds__(64 * NW) void gated_bwd_kernel(GatedArgs a) {
           st[v] = rs ? b : fmaf(da[j][v], st[v], b);
         }
       }
+      if (later > 0)
+        min = entering<RESET>(looked, a.ws_maps, a.ws_ends, later, [&](int64_t k) { return slot + k * plane; }, on,
+                                  q.wave, q.lane);
+      if (q.wave == 0 && on) {
+        const float mout = after<RESET>(pt, mt, min);
+        if (a.ntiles > 1) publish(a.ws_ends + slot, word(0, mout));
+        if (a.dh0 != nullptr && q.tile == 0) a.dh0[at] = mout;
+        enter[q.lane] = min;
+      }
       lds_sync();
 #pragma unroll
       for (int v = 0; v < V; ++v) ms[v] = enter[q.col * V + v];
+#pragma unroll 1
       for (int w = NW - 1; w > q.wave; --w)
 #pragma unroll
         for (int v = 0; v < V; ++v) ms[v] = after<RESET>(tot[w][q.col * V + v].x, tom[w][q.col * V + v], ms[v]);
 #pragma unroll
       for (int v = 0; v < V; ++v) ms[v] = after<RESET>(qe[v], me[v], ms[v]);
     }
-    Raw<BF16, V> ox[K], og[K], oi[K];
+    if (!q.active) return;
+    const Rows<BF16, V> ox(a.dx, first, off, step), og(a.dr, first, off, step), oi(a.di, first, off, step);
+    // token after token: mixed, their parts that do not wait for lam would all be held at once
 #pragma unroll
     for (int j = K - 1; j >= 0; --j) {
       const bool rs = RESET && ((resets >> j) & 1u);
       float dx[V], dg[V], di[V];
+      forget(rx[j]);
+      forget(rd[j]);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float x = rx[j].get(v), lam = ms[v] + rd[j].get(v);
@@ -640,14 +636,11 @@ __global__ __launch_bounds__(64 * NW) void gated_bwd_kernel(GatedArgs a) {
         if (!FF) dec = j < nv ? dec : 1.f;
         ms[v] = rs ? 0.f : dec * lam;
       }
-      ox[j] = Raw<BF16, V>::make(dx);
-      og[j] = Raw<BF16, V>::make(dg);
-      oi[j] = Raw<BF16, V>::make(di);
-    }
-    if (q.active) {
-      store_run<BF16, V, K, FF>(a.dx, first, step, off, nv, ox);
-      store_run<BF16, V, K, FF>(a.dr, first, step, off, nv, og);
-      if (FORM == kGatedLru) store_run<BF16, V, K, FF>(a.di, first, step, off, nv, oi);
+      if (FF || j < nv) {
+        ox.store(j, Raw<BF16, V>::make(dx));
+        og.store(j, Raw<BF16, V>::make(dg));
+        if (FORM == kGatedLru) oi.store(j, Raw<BF16, V>::make(di));
+      }
     }
   };
   if ((FORM != kGatedLru || __all(near1)) && q.t0 + T <= L) run(std::true_type{});
@@ -724,34 +717,27 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedArgs a) {
   *reinterpret_cast<R*>((char*)a.y + k * es) = R::make(st);
 }
 
-constexpr int run_len(bool bf16) { return bf16 ? KF : 8; }   // tokens of a lane's run, forward
-constexpr int kRunBwd = KB;
-
-template <bool BF16, int V, int FORM, bool RESET, int NW>
-void launch(const GatedArgs& a, unsigned grid, bool bwd, hipStream_t st) {
-  if (bwd) gated_bwd_kernel<BF16, V, FORM, RESET, kRunBwd, NW><<<grid, 64 * NW, 0, st>>>(a);
-  else gated_fwd_kernel<BF16, V, FORM, RESET, run_len(BF16), NW><<<grid, 64 * NW, 0, st>>>(a);
-}
+// Tokens of a lane's run: what four waves a SIMD leave registers for.
+constexpr int run_len(bool bf16, bool bwd) { return (bf16 ? 16 : 8) / (bwd ? 2 : 1); }
 
 // Instances: V = 2 where the rows allow it, with and without resets; the
 // one-channel kernels always look for them.
 template <bool BF16, int V, int FORM, bool RESET>
-void pick(const GatedArgs& a, unsigned grid, int waves, bool bwd, hipStream_t st) {
-  if (waves == 4) launch<BF16, V, FORM, RESET, 4>(a, grid, bwd, st);
-  else if (waves == 8) launch<BF16, V, FORM, RESET, 8>(a, grid, bwd, st);
-  else launch<BF16, V, FORM, RESET, 16>(a, grid, bwd, st);
+void launch(const GatedArgs& a, unsigned grid, bool bwd, hipStream_t st) {
+  if (bwd) gated_bwd_kernel<BF16, V, FORM, RESET, run_len(BF16, true)><<<grid, 64 * NW, 0, st>>>(a);
+  else gated_fwd_kernel<BF16, V, FORM, RESET, run_len(BF16, false)><<<grid, 64 * NW, 0, st>>>(a);
 }
 template <bool BF16, int FORM>
-void pick(const GatedArgs& a, unsigned grid, int waves, bool bwd, hipStream_t st) {
-  if (!a.vec) pick<BF16, 1, FORM, true>(a, grid, waves, bwd, st);
-  else if (a.reset != nullptr) pick<BF16, 2, FORM, true>(a, grid, waves, bwd, st);
-  else pick<BF16, 2, FORM, false>(a, grid, waves, bwd, st);
+void pick(const GatedArgs& a, unsigned grid, bool bwd, hipStream_t st) {
+  if (!a.vec) launch<BF16, 1, FORM, true>(a, grid, bwd, st);
+  else if (a.reset != nullptr) launch<BF16, 2, FORM, true>(a, grid, bwd, st);
+  else launch<BF16, 2, FORM, false>(a, grid, bwd, st);
 }
-void pick(const GatedArgs& a, unsigned grid, int waves, bool bwd, hipStream_t st) {
+void pick(const GatedArgs& a, unsigned grid, bool bwd, hipStream_t st) {
   if (a.act_bf16) {
-    a.form == kGatedLru ? pick<true, kGatedLru>(a, grid, waves, bwd, st) : pick<true, kGatedUnit>(a, grid, waves, bwd, st);
+    a.form == kGatedLru ? pick<true, kGatedLru>(a, grid, bwd, st) : pick<true, kGatedUnit>(a, grid, bwd, st);
   } else {
-    a.form == kGatedLru ? pick<false, kGatedLru>(a, grid, waves, bwd, st) : pick<false, kGatedUnit>(a, grid, waves, bwd, st);
+    a.form == kGatedLru ? pick<false, kGatedLru>(a, grid, bwd, st) : pick<false, kGatedUnit>(a, grid, bwd, st);
   }
 }
 
@@ -762,13 +748,11 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // Columns: as many lanes across the channels as there are channels for, up to 32 (a 128-byte row of bf16
 // pairs); the other lanes go along time.
 GatedPlan plan_gated(int64_t batch, int64_t seqlen, int64_t dim, bool bf16, bool bwd) {
-  GatedPlan p{4, 8, 0, 1, 0, 0, 0};
+  GatedPlan p{4, 0, 1, 0, 0, 0};
   if (batch == 0 || dim == 0) return p;
   const int V = dim % 2 == 0 ? 2 : 1;
   while (p.cols < kGatedMaxCols && (int64_t)p.cols * V < dim) p.cols *= 2;
-  if (const char* e = getenv("GW")) p.waves = atoi(e);
-  if (const char* e = getenv("GC")) p.cols = atoi(e);
-  p.tile = (int64_t)p.waves * (64 / p.cols) * (bwd ? kRunBwd : run_len(bf16));
+  p.tile = (int64_t)NW * (64 / p.cols) * run_len(bf16, bwd);
   p.ntiles = std::max<int64_t>(1, (seqlen + p.tile - 1) / p.tile);
   const size_t plane = (size_t)(batch * dim);
   p.words_bytes = p.ntiles > 1 ? up256(2 * p.ntiles * plane * sizeof(uint64_t)) + 256 : 0;
@@ -793,7 +777,7 @@ static int run_pass(GatedArgs a, const GatedPlan& p, bool bwd, void* ws, hipStre
     a.ws_ends = a.ws_maps + words / 2;
     gated_clear_kernel<<<(unsigned)blocks, 256, 0, st>>>(a.ws_maps, words, a.ws_count);
   }
-  pick(a, (unsigned)n, p.waves, bwd, st);
+  pick(a, (unsigned)n, bwd, st);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? 0 : fail(6, std::string("gated scan launch: ") + hipGetErrorString(e));
 }

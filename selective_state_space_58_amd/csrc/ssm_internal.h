@@ -271,7 +271,7 @@ struct GatedArgs {
 };
 
 struct GatedPlan {
-  int cols, waves;             // lanes across channels; waves of a workgroup
+  int cols;                    // lanes across channels
   int64_t tile, ntiles;        // tokens of a tile
   size_t words_bytes, da_bytes, states_bytes;
 };
