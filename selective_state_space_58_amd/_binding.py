@@ -1,7 +1,9 @@
 """ctypes marshalling for libssm_mi355x.so (argument checks and pointers only)."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -135,7 +137,7 @@ def _check(lib, fn, rc):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t, name, dtype=None, shape=None, device=None):
@@ -151,13 +153,13 @@ def _need(t, name, dtype=None, shape=None, device=None):
         raise ValueError("%s must be contiguous" % name)
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     return t
 
 
 def _stream(dev):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _act_code(t, name):
@@ -532,15 +534,25 @@ SSM_GATED_LRU = 0
 SSM_GATED_UNIT = 1
 
 
+_HERE_ALREADY = contextlib.nullcontext()
+
+
 def _on(dev):
     """The library's kernels run on the current device: make it the tensors'."""
-    return torch.cuda.device(dev)
+    return _HERE_ALREADY if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
-def _workspace(workspace, nbytes, dev):
+@functools.lru_cache(maxsize=4096)
+def _bytes(name, device_index, *sizes):
+    """A *_workspace_bytes query (its answer goes by the sizes and the current device alone)."""
+    return int(getattr(load_library(), name)(*sizes))
+
+
+def _workspace(workspace, query, dev, *sizes):
     """The caller's workspace, checked, or one of torch's (from its stream-ordered pool, so that a call
-    under graph capture takes the graph's own)."""
+    under graph capture takes the graph's own) of the bytes that the query gives for these sizes."""
     if workspace is None:
+        nbytes = _bytes(query, dev.index, *sizes)
         return (torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes) if nbytes > 0 else (None, 0)
     _need(workspace, "workspace", device=dev)
     return workspace, workspace.numel() * workspace.element_size()
@@ -576,7 +588,7 @@ def ssm_causal_conv1d_bwd(x, weight, dout, bias=None, state_in=None, silu=True, 
             g["dbias"] = torch.empty_like(bias)
         if state_in is not None or want_dstate_in:
             g["dstate_in"] = torch.empty((batch, dim, width - 1), dtype=x.dtype, device=dev)
-        ws, wsb = _workspace(workspace, ssm_causal_conv1d_bwd_workspace_bytes(batch, seqlen, dim, width), dev)
+        ws, wsb = _workspace(workspace, "ssm_causal_conv1d_bwd_workspace_bytes", dev, batch, seqlen, dim, width)
         rc = lib.ssm_causal_conv1d_bwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(state_in), int(bool(silu)), _ptr(dout),
                                        _ptr(dstate_out), _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(g.get("dbias")),
                                        _ptr(g.get("dstate_in")), batch, seqlen, dim, width, act, _ptr(ws), wsb,
@@ -656,7 +668,7 @@ def _gated_fwd(name, x, r, i, A, reset, h0, return_final_state, y, h_final, stat
         if return_final_state and h_final is None:
             h_final = torch.empty((batch, dim), dtype=torch.float32, device=dev)
         _need(h_final, "h_final", torch.float32, (batch, dim), dev)
-        ws, wsb = _workspace(workspace, lib.ssm_gated_scan_workspace_bytes(batch, seqlen, dim, act), dev)
+        ws, wsb = _workspace(workspace, "ssm_gated_scan_workspace_bytes", dev, batch, seqlen, dim, act)
         rc = lib.ssm_gated_scan_fwd(_ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(reset), _ptr(h0), _ptr(y), _ptr(h_final),
                                     _ptr(states), batch, seqlen, dim, form, act, _ptr(ws), wsb, _stream(dev))
     _check(lib, name, rc)
@@ -684,7 +696,7 @@ def ssm_gated_scan_bwd(x, r, dout, i=None, A=None, reset=None, h0=None, dh_final
         if h0 is not None or want_dh0:
             g["dh0"] = torch.empty((batch, dim), dtype=torch.float32, device=dev)
         have = int(states is not None and states.numel() > 0)
-        ws, wsb = _workspace(workspace, lib.ssm_gated_scan_bwd_workspace_bytes(batch, seqlen, dim, act, have), dev)
+        ws, wsb = _workspace(workspace, "ssm_gated_scan_bwd_workspace_bytes", dev, batch, seqlen, dim, act, have)
         rc = lib.ssm_gated_scan_bwd(_ptr(x), _ptr(r), _ptr(i), _ptr(A), _ptr(reset), _ptr(h0),
                                     _ptr(states) if have else None, _ptr(dout), _ptr(dh_final), _ptr(g["dx"]),
                                     _ptr(g["dr"]), _ptr(g.get("di")), _ptr(g.get("dA")), _ptr(g.get("dh0")),
@@ -784,7 +796,7 @@ def ssm_block_norm_bwd(y, dres=None, dout=None, z=None, residual=None, w_post=No
         for t, name in ((w_post, "dw_post"), (scale, "dscale"), (w_pre, "dw_pre")):
             if t is not None:
                 g[name] = torch.empty_like(t)
-        ws, wsb = _workspace(workspace, ssm_block_norm_bwd_workspace_bytes(rows, dim), dev)
+        ws, wsb = _workspace(workspace, "ssm_block_norm_bwd_workspace_bytes", dev, rows, dim)
         rc = lib.ssm_block_norm_bwd(_ptr(y), _ptr(z), _ptr(residual), _ptr(w_post), _ptr(scale), _ptr(w_pre), _ptr(rng),
                                     p, eps, _ptr(dres), _ptr(dout), _ptr(g["dy"]), _ptr(g.get("dz")),
                                     _ptr(g.get("dresidual")), _ptr(g.get("dw_post")), _ptr(g.get("dscale")),

@@ -717,8 +717,6 @@ static int norm_common(NormArgs& a, const void* y, const void* z, const void* re
   a.y = y; a.z = z; a.residual = residual; a.w_post = w_post; a.scale = scale; a.w_pre = w_pre; a.rng = rng;
   a.rows = rows; a.dim = dim; a.eps = eps; a.drop = drop; a.keep_scale = 65536.f / (65536.f - (float)drop);
   a.act_bf16 = act_dtype == SSM_BF16; a.res_bf16 = res_dtype == SSM_BF16;
-  a.vec = dim % 8 == 0 && aligned16(y) && aligned16(z) && aligned16(residual) && aligned16(w_post) &&
-          aligned16(scale) && aligned16(w_pre);
   return SSM_OK;
 }
 
@@ -743,13 +741,12 @@ int ssm_block_norm_fwd(const void* y, const void* z, const void* residual, const
       (res_out != residual && overlap(res_out, n * rs, residual, n * rs)))
     return fail(SSM_ERR_SHAPE, "outputs must not overlap inputs (res_out may be residual)");
   a.res_out = res_out; a.out = out;
-  a.vec = a.vec && aligned16(res_out) && aligned16(out);
   return launch_norm_fwd(a, stream);
 }
 
 size_t ssm_block_norm_bwd_workspace_bytes(int64_t rows, int64_t dim) {
   if (rows <= 0 || dim <= 0 || dim > kNormMaxDim || !elems_ok({rows, dim})) return 0;
-  return norm_bwd_ws_bytes(rows, dim);
+  return norm_bwd_ws_bytes(rows, dim, device_cu_count());
 }
 
 int ssm_block_norm_bwd(const void* y, const void* z, const void* residual, const float* w_post, const float* scale,
@@ -790,8 +787,7 @@ int ssm_block_norm_bwd(const void* y, const void* z, const void* residual, const
   a.dw_post = w_post != nullptr ? dw_post : nullptr;
   a.dscale = scale != nullptr ? dscale : nullptr;
   a.dw_pre = w_pre != nullptr ? dw_pre : nullptr;
-  a.vec = a.vec && aligned16(dres) && aligned16(dout) && aligned16(dy) && aligned16(a.dz) && aligned16(a.dresidual);
-  return launch_norm_bwd(a, stream);
+  return launch_norm_bwd(a, device_cu_count(), stream);
 }
 
 }  // extern "C"

@@ -56,55 +56,83 @@ __device__ __forceinline__ unsigned keep_bits(uint64_t q, const int64_t* rng, un
   return m;
 }
 
-// Which columns a thread holds: pack j is 8 consecutive columns (VEC), or 8
-// columns tpr apart, each loaded by itself.
-template <bool VEC>
-struct Cols {
-  int tid, tpr;   // thread of the row, threads of a row
-  int64_t dim;
-  __device__ __forceinline__ int64_t at(int j, int e) const {
-    return VEC ? ((int64_t)j * tpr + tid) * 8 + e : ((int64_t)j * 8 + e) * tpr + tid;
+// A pack of eight consecutive columns as it lies in memory.  Rows need not be
+// aligned: the 16-byte accesses are marked so.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+template <bool BF16>
+struct Pack {
+  u32x4 u[BF16 ? 1 : 2];
+  __device__ __forceinline__ float get(int e) const {
+    if (BF16) return e % 2 == 0 ? bf16_lo(u[0][e / 2]) : bf16_hi(u[0][e / 2]);
+    const unsigned w = u[BF16 ? 0 : e / 4][e % 4];   // (a scalar first: bit_cast takes no vector element)
+    return __builtin_bit_cast(float, w);
   }
-  __device__ __forceinline__ bool in(int j, int e) const { return at(j, VEC ? 0 : e) < dim; }
-};
-
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void load_pack(const void* p, int64_t row, const Cols<VEC>& c, int j, float (&v)[8]) {
-  if constexpr (VEC) {
-    if (c.in(j, 0)) {
-      load8<BF16>(p, row + c.at(j, 0), v);
+  static __device__ __forceinline__ Pack make(const float (&v)[8]) {
+    Pack p;
+    if constexpr (BF16) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) p.u[0][q] = pack_bf16(v[2 * q], v[2 * q + 1]);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+      for (int e = 0; e < 8; ++e) p.u[e / 4][e % 4] = __builtin_bit_cast(unsigned, v[e]);
     }
+    return p;
+  }
+};
+
+// Pack j of a thread: columns (j tpr + tid) 8 and the seven after it; n of them
+// are in the row.
+struct Cols {
+  int tid, tpr, dim;   // thread of the row, threads of a row
+  __device__ __forceinline__ int at(int j) const { return (j * tpr + tid) * 8; }
+  __device__ __forceinline__ int n(int j) const { return dim - at(j); }
+};
+template <bool BF16>
+__device__ __forceinline__ Pack<BF16> load_raw(const void* p, int64_t row, const Cols& c, int j) {
+  Pack<BF16> r = {};
+  const char* q = (const char*)p + (row + c.at(j)) * (BF16 ? 2 : 4);
+  if (c.n(j) >= 8) {
+    r.u[0] = *reinterpret_cast<const u32x4_any*>(q);
+    if (!BF16) r.u[BF16 ? 0 : 1] = *reinterpret_cast<const u32x4_any*>(q + 16);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c.in(j, e) ? load1<BF16>(p, row + c.at(j, e)) : 0.f;
+    for (int e = 0; e < 7; ++e)
+      if (e < c.n(j)) {
+        if (BF16) r.u[0][e / 2] |= (unsigned)((const unsigned short*)q)[e] << (16 * (e % 2));
+        else r.u[BF16 ? 0 : e / 4][e % 4] = ((const unsigned*)q)[e];
+      }
+  }
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ void load_pack(const void* p, int64_t row, const Cols& c, int j, float (&v)[8]) {
+  const Pack<BF16> r = load_raw<BF16>(p, row, c, j);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = r.get(e);
+}
+template <bool BF16>
+__device__ __forceinline__ void store_pack(void* p, int64_t row, const Cols& c, int j, const float (&v)[8]) {
+  const Pack<BF16> r = Pack<BF16>::make(v);
+  char* q = (char*)p + (row + c.at(j)) * (BF16 ? 2 : 4);
+  if (c.n(j) >= 8) {
+    *reinterpret_cast<u32x4_any*>(q) = r.u[0];
+    if (!BF16) *reinterpret_cast<u32x4_any*>(q + 16) = r.u[BF16 ? 0 : 1];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (e < c.n(j)) {
+        if (BF16) ((unsigned short*)q)[e] = (unsigned short)(r.u[0][e / 2] >> (16 * (e % 2)));
+        else ((unsigned*)q)[e] = r.u[BF16 ? 0 : e / 4][e % 4];
+      }
   }
 }
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void store_pack(void* p, int64_t row, const Cols<VEC>& c, int j, const float (&v)[8]) {
-  if constexpr (VEC) {
-    if (c.in(j, 0)) store8<BF16>(p, row + c.at(j, 0), v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c.in(j, e)) store1<BF16>(p, row + c.at(j, e), v[e]);
-  }
-}
-template <bool VEC>
-__device__ __forceinline__ unsigned keep_pack(const NormArgs& a, int64_t row, const Cols<VEC>& c, int j) {
-  if constexpr (VEC) {
-    return keep_bits((uint64_t)(row + c.at(j, 0)) >> 3, a.rng, a.drop);
-  } else {
-    unsigned m = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint64_t i = (uint64_t)(row + c.at(j, e));
-      m |= ((keep_bits(i >> 3, a.rng, a.drop) >> (i & 7)) & 1u) << e;
-    }
-    return m;
-  }
+// Keep bits of a pack; in rows that do not start at a whole block it lies in two of them.
+__device__ __forceinline__ unsigned keep_pack(const NormArgs& a, int64_t row, const Cols& c, int j) {
+  const uint64_t e = (uint64_t)(row + c.at(j));
+  unsigned m = keep_bits(e >> 3, a.rng, a.drop);
+  const unsigned shift = (unsigned)(e & 7);
+  if (shift != 0) m = (m | keep_bits((e >> 3) + 1, a.rng, a.drop) << 8) >> shift;
+  return m;
 }
 
 // Sums N values over the threads of a row, the same order for every thread.
@@ -133,23 +161,23 @@ __device__ __forceinline__ void row_sum(float (&s)[N], int tpr, float (*red)[N],
   }
 }
 
-template <bool BF16, bool RBF16, bool VEC, int NV>
+template <bool BF16, bool RBF16, int NV>
 __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a) {
   __shared__ float red[2 * kMaxWaves][1];
   const int rpb = blockDim.x / a.tpr;
   const int64_t r = (int64_t)blockIdx.x * rpb + threadIdx.x / a.tpr;
   const bool live = r < a.rows;
-  const Cols<VEC> c{(int)(threadIdx.x % a.tpr), a.tpr, live ? a.dim : 0};
+  const Cols c{(int)(threadIdx.x % a.tpr), a.tpr, live ? (int)a.dim : 0};
   const int64_t row = live ? r * a.dim : 0;
   const float inv = 1.f / (float)a.dim;
   int buf = 0;
   float v[NV][8], s[1] = {0.f};
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    load_pack<BF16, VEC>(a.y, row, c, j, v[j]);
+    load_pack<BF16>(a.y, row, c, j, v[j]);
     if (a.z != nullptr) {
       float z[8];
-      load_pack<BF16, VEC>(a.z, row, c, j, z);
+      load_pack<BF16>(a.z, row, c, j, z);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[j][e] *= z[e] * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-z[e] * kLog2e));
     }
@@ -162,7 +190,7 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float w[8];
-      load_pack<false, VEC>(a.w_post, 0, c, j, w);
+      load_pack<false>(a.w_post, 0, c, j, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[j][e] *= r1 * w[e];
     }
@@ -172,22 +200,22 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a) {
   for (int j = 0; j < NV; ++j) {
     if (a.scale != nullptr) {
       float w[8];
-      load_pack<false, VEC>(a.scale, 0, c, j, w);
+      load_pack<false>(a.scale, 0, c, j, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[j][e] *= w[e];
     }
     if (a.drop != 0) {
-      const unsigned m = keep_pack<VEC>(a, row, c, j);
+      const unsigned m = keep_pack(a, row, c, j);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[j][e] = (m >> e) & 1u ? v[j][e] * a.keep_scale : 0.f;
     }
     if (a.residual != nullptr) {
       float q[8];
-      load_pack<RBF16, VEC>(a.residual, row, c, j, q);
+      load_pack<RBF16>(a.residual, row, c, j, q);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[j][e] += q[e];
     }
-    if (a.res_out != nullptr) store_pack<RBF16, VEC>(a.res_out, row, c, j, v[j]);
+    if (a.res_out != nullptr) store_pack<RBF16>(a.res_out, row, c, j, v[j]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[0] = fmaf(v[j][e], v[j][e], s[0]);
   }
@@ -197,43 +225,12 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float w[8];
-      load_pack<false, VEC>(a.w_pre, 0, c, j, w);
+      load_pack<false>(a.w_pre, 0, c, j, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] *= v[j][e] * r2;
-      store_pack<BF16, VEC>(a.out, row, c, j, w);
+      store_pack<BF16>(a.out, row, c, j, w);
     }
   }
-}
-
-// A pack as it lies in memory, for values that wait while a row is summed.
-template <bool BF16>
-struct Pack {
-  u32x4 u[BF16 ? 1 : 2];
-  __device__ __forceinline__ float get(int e) const {
-    if (BF16) return e % 2 == 0 ? bf16_lo(u[0][e / 2]) : bf16_hi(u[0][e / 2]);
-    const unsigned w = u[BF16 ? 0 : e / 4][e % 4];   // (a scalar first: bit_cast takes no vector element)
-    return __builtin_bit_cast(float, w);
-  }
-};
-template <bool BF16, bool VEC>
-__device__ __forceinline__ Pack<BF16> load_raw(const void* p, int64_t row, const Cols<VEC>& c, int j) {
-  Pack<BF16> r = {};
-  if constexpr (VEC) {
-    if (c.in(j, 0)) {
-      const u32x4* q = reinterpret_cast<const u32x4*>((const char*)p + (row + c.at(j, 0)) * (BF16 ? 2 : 4));
-      r.u[0] = q[0];
-      if (!BF16) r.u[BF16 ? 0 : 1] = q[1];
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (c.in(j, e)) {
-        if (BF16) r.u[0][e / 2] |= (unsigned)((const unsigned short*)p)[row + c.at(j, e)] << (16 * (e % 2));
-        else r.u[BF16 ? 0 : e / 4][e % 4] = ((const unsigned*)p)[row + c.at(j, e)];
-      }
-    }
-  }
-  return r;
 }
 
 // Gradient.  With vhat = v / rms(v), Rhat = R / rms(R), q = dout w_pre, w = w_post scale:
@@ -241,9 +238,33 @@ __device__ __forceinline__ Pack<BF16> load_raw(const void* p, int64_t row, const
 //   dv = (dn - vhat mean(dn vhat)) / rms(v)
 //   dw_post = scale S, dscale = w_post S with S = sum_rows dm vhat;  dw_pre = sum_rows dout Rhat
 // A workgroup walks rows that lie gridDim.x apart and keeps its share of S and
-// dw_pre in registers.
-template <bool BF16, bool RBF16, bool VEC, int NV, int MAXT>
-__global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a) {
+// dw_pre in registers.  AHEAD: the next row's loads are issued before the present
+// row's sums, whose three rounds of waiting they fill.
+template <bool BF16, bool RBF16, int NV>
+struct Row {
+  Pack<BF16> y[NV], z[NV], dout[NV];
+  Pack<RBF16> res[NV], dres[NV];
+  __device__ __forceinline__ void load(const NormArgs& a, int64_t row, const Cols& c) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      y[j] = load_raw<BF16>(a.y, row, c, j);
+      if (a.z != nullptr) z[j] = load_raw<BF16>(a.z, row, c, j);
+      if (a.w_pre != nullptr) {
+        if (a.residual != nullptr) res[j] = load_raw<RBF16>(a.residual, row, c, j);
+        dout[j] = load_raw<BF16>(a.dout, row, c, j);
+      }
+      if (a.dres != nullptr) dres[j] = load_raw<RBF16>(a.dres, row, c, j);
+    }
+  }
+};
+// Hides that a pack was unpacked before, so that it is kept packed and unpacked again.
+template <bool BF16>
+__device__ __forceinline__ void forget(Pack<BF16>& p) {
+  if (BF16) asm("" : "+v"(p.u[0]));
+}
+
+template <bool BF16, bool RBF16, int NV, int MAXT, int WAVES, bool AHEAD>
+__global__ __launch_bounds__(MAXT, WAVES) void norm_bwd_kernel(NormArgs a) {
   __shared__ float red1[2 * kMaxWaves][1];
   __shared__ float red2[2 * kMaxWaves][2];
   const int rpb = blockDim.x / a.tpr;
@@ -252,7 +273,7 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a) {
   int buf1 = 0, buf2 = 0;
   float gs[NV][8], gpre[NV][8], w[NV][8], wpre[NV][8];
   {
-    const Cols<VEC> c{tid, a.tpr, a.dim};
+    const Cols c{tid, a.tpr, (int)a.dim};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
@@ -260,37 +281,32 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a) {
         gs[j][e] = gpre[j][e] = wpre[j][e] = 0.f;
         w[j][e] = 1.f;
       }
-      if (a.w_post != nullptr) load_pack<false, VEC>(a.w_post, 0, c, j, w[j]);
+      if (a.w_post != nullptr) load_pack<false>(a.w_post, 0, c, j, w[j]);
       if (a.scale != nullptr) {
         float sc[8];
-        load_pack<false, VEC>(a.scale, 0, c, j, sc);
+        load_pack<false>(a.scale, 0, c, j, sc);
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[j][e] *= sc[e];
       }
-      if (a.w_pre != nullptr) load_pack<false, VEC>(a.w_pre, 0, c, j, wpre[j]);
+      if (a.w_pre != nullptr) load_pack<false>(a.w_pre, 0, c, j, wpre[j]);
     }
   }
 
-  for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < a.rows; r0 += (int64_t)gridDim.x * rpb) {
-    const int64_t r = r0 + threadIdx.x / a.tpr;
-    const bool live = r < a.rows;
-    const Cols<VEC> c{tid, a.tpr, live ? a.dim : 0};
-    const int64_t row = live ? r * a.dim : 0;
-    Pack<BF16> y[NV], z[NV], dout[NV];
-    Pack<RBF16> res[NV], dres[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      y[j] = load_raw<BF16, VEC>(a.y, row, c, j);
-      z[j] = {};
-      res[j] = {};
-      dout[j] = {};
-      dres[j] = {};
-      if (a.z != nullptr) z[j] = load_raw<BF16, VEC>(a.z, row, c, j);
-      if (a.w_pre != nullptr) {
-        if (a.residual != nullptr) res[j] = load_raw<RBF16, VEC>(a.residual, row, c, j);
-        dout[j] = load_raw<BF16, VEC>(a.dout, row, c, j);
-      }
-      if (a.dres != nullptr) dres[j] = load_raw<RBF16, VEC>(a.dres, row, c, j);
+  const int64_t stride = (int64_t)gridDim.x * rpb;
+  int64_t r = (int64_t)blockIdx.x * rpb + threadIdx.x / a.tpr;
+  auto cols_of = [&](int64_t r) { return Cols{tid, a.tpr, r < a.rows ? (int)a.dim : 0}; };
+  Row<BF16, RBF16, NV> next = {};
+  if (AHEAD) next.load(a, r < a.rows ? r * a.dim : 0, cols_of(r));
+  // (a workgroup's rows are walked together: the sums meet at barriers)
+  for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < a.rows; r0 += stride, r += stride) {
+    const Cols c = cols_of(r);
+    const int64_t row = r < a.rows ? r * a.dim : 0;
+    Row<BF16, RBF16, NV> q = {};
+    if (AHEAD) {
+      q = next;
+      if (r0 + stride < a.rows) next.load(a, r + stride < a.rows ? (r + stride) * a.dim : 0, cols_of(r + stride));
+    } else {
+      q.load(a, row, c);
     }
     float v[NV][8], R[NV][8];   // R: then dn
     unsigned keep[NV];
@@ -299,14 +315,14 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a) {
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        v[j][e] = y[j].get(e);
+        v[j][e] = q.y[j].get(e);
         if (a.z != nullptr) {
-          const float zz = z[j].get(e);
+          const float zz = q.z[j].get(e);
           v[j][e] *= zz * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-zz * kLog2e));
         }
         s1[0] = fmaf(v[j][e], v[j][e], s1[0]);
       }
-      keep[j] = a.drop != 0 ? keep_pack<VEC>(a, row, c, j) : 0xffu;
+      keep[j] = a.drop != 0 ? keep_pack(a, row, c, j) : 0xffu;
     }
     float r1 = 1.f;
     if (a.w_post != nullptr) {
@@ -321,9 +337,9 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a) {
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          R[j][e] = res[j].get(e) + ((keep[j] >> e) & 1u ? v[j][e] * rk * w[j][e] : 0.f);
+          R[j][e] = q.res[j].get(e) + ((keep[j] >> e) & 1u ? v[j][e] * rk * w[j][e] : 0.f);
           s2[0] = fmaf(R[j][e], R[j][e], s2[0]);
-          s2[1] = fmaf(R[j][e], dout[j].get(e) * wpre[j][e], s2[1]);
+          s2[1] = fmaf(R[j][e], q.dout[j].get(e) * wpre[j][e], s2[1]);
         }
       row_sum<2>(s2, a.tpr, red2, buf2);
       r2 = __builtin_amdgcn_rsqf(fmaf(s2[0], inv, a.eps));
@@ -338,13 +354,14 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float dR[8];
+      forget(q.dout[j]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = dout[j].get(e);
+        const float d = q.dout[j].get(e);
         gpre[j][e] = fmaf(d, R[j][e] * r2, gpre[j][e]);
-        dR[e] = fmaf(r2, fmaf(-k2, R[j][e], d * wpre[j][e]), dres[j].get(e));
+        dR[e] = fmaf(r2, fmaf(-k2, R[j][e], d * wpre[j][e]), q.dres[j].get(e));
       }
-      if (a.dresidual != nullptr) store_pack<RBF16, VEC>(a.dresidual, row, c, j, dR);
+      if (a.dresidual != nullptr) store_pack<RBF16>(a.dresidual, row, c, j, dR);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float dm = (keep[j] >> e) & 1u ? dR[e] * a.keep_scale : 0.f;
@@ -365,20 +382,22 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a) {
       for (int e = 0; e < 8; ++e) dv[e] = r1 * fmaf(-k, v[j][e], R[j][e]);
       if (a.z != nullptr) {
         float dz[8];
+        forget(q.y[j]);
+        forget(q.z[j]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float zz = z[j].get(e);
+          const float zz = q.z[j].get(e);
           const float sg = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-zz * kLog2e));
-          dz[e] = dv[e] * y[j].get(e) * sg * fmaf(zz, 1.f - sg, 1.f);
+          dz[e] = dv[e] * q.y[j].get(e) * sg * fmaf(zz, 1.f - sg, 1.f);
           dv[e] *= zz * sg;
         }
-        store_pack<BF16, VEC>(a.dz, row, c, j, dz);
+        store_pack<BF16>(a.dz, row, c, j, dz);
       }
-      store_pack<BF16, VEC>(a.dy, row, c, j, dv);
+      store_pack<BF16>(a.dy, row, c, j, dv);
     }
   }
 
-  // rows of the wave, then one part per wave (rows within a wave) or per workgroup
+  // rows of the wave, then, where a row is no more than a wave, the waves: one part a workgroup
   for (int sh = a.tpr; sh < 64; sh <<= 1)
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -387,30 +406,56 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs a) {
         gs[j][e] += __shfl_xor(gs[j][e], sh);
         gpre[j][e] += __shfl_xor(gpre[j][e], sh);
       }
-  const Cols<VEC> c{tid, a.tpr, (int)(threadIdx.x & 63) < a.tpr ? a.dim : 0};
-  const int64_t part = a.tpr <= 64 ? (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6) : blockIdx.x;
+  bool writes = true;
+  if constexpr (NV == 1) {
+    if (a.tpr <= 64) {
+      __shared__ float sums[3][16][64];
+      const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+      if (wave > 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          sums[wave - 1][e][lane] = gs[0][e];
+          sums[wave - 1][8 + e][lane] = gpre[0][e];
+        }
+      }
+      lds_sync();
+      for (int o = 0; o < 3; ++o)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          gs[0][e] += sums[o][e][lane];
+          gpre[0][e] += sums[o][8 + e][lane];
+        }
+      writes = threadIdx.x < (unsigned)a.tpr;
+    }
+  }
+  const Cols c{tid, a.tpr, writes ? (int)a.dim : 0};
+  const int64_t part = blockIdx.x;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    store_pack<false, VEC>(a.ws, part * 2 * a.dim, c, j, gs[j]);
-    store_pack<false, VEC>(a.ws, (part * 2 + 1) * a.dim, c, j, gpre[j]);
+    store_pack<false>(a.ws, part * 2 * a.dim, c, j, gs[j]);
+    store_pack<false>(a.ws, (part * 2 + 1) * a.dim, c, j, gpre[j]);
   }
 }
 
-// The weight gradients from the parts of S and dw_pre: 32 columns by 8 slices of the parts.
-__global__ __launch_bounds__(256) void norm_sum_kernel(NormArgs a, int64_t nparts) {
-  __shared__ float red[8][32];
+// The weight gradients from the parts of S and dw_pre, in a fixed order: 32
+// columns by 32 slices of the parts, four parts read at a time.
+__global__ __launch_bounds__(1024) void norm_sum_kernel(NormArgs a, int64_t nparts) {
+  __shared__ float red[32][33];
   const int col = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + col;
   const int which = blockIdx.y;   // 0: S, 1: dw_pre
+  const float* src = a.ws + which * a.dim + c;
   float s = 0.f;
-  if (c < a.dim)
-    for (int64_t p = slice; p < nparts; p += 8) s += a.ws[(p * 2 + which) * a.dim + c];
+  if (c < a.dim) {
+#pragma unroll 4
+    for (int64_t p = slice; p < nparts; p += 32) s += src[p * 2 * a.dim];
+  }
   red[slice][col] = s;
   lds_sync();
   if (slice != 0 || c >= a.dim) return;
   s = 0.f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) s += red[k][col];
+  for (int k = 0; k < 32; ++k) s += red[k][col];
   if (which == 1) {
     if (a.dw_pre != nullptr) a.dw_pre[c] = s;
   } else {
@@ -428,51 +473,42 @@ int threads_per_row(int64_t dim, int NV) {
   return packs <= 64 ? t : (int)((packs + 63) / 64 * 64);
 }
 int packs_fwd(int64_t dim) { return dim <= 8 * 64 ? 1 : 2; }
-int packs_bwd(int64_t dim) { return dim <= 8 * 512 ? 1 : 2; }
-constexpr int64_t kBwdGroups = 512;   // workgroups of the backward at most
 
+// Backward: one pack a thread to 768 threads (three waves a SIMD, 168 registers), in bf16 with the next row's
+// loads ahead; wider rows two packs a thread.
 struct BwdShape {
   int NV, tpr, threads;
-  int64_t grid, parts;
+  int64_t grid;
 };
-BwdShape bwd_shape(int64_t rows, int64_t dim) {
+constexpr int64_t kAheadDim = 8 * 768;
+BwdShape bwd_shape(int64_t rows, int64_t dim, int num_cus) {
   BwdShape s;
-  s.NV = packs_bwd(dim);
+  s.NV = dim <= kAheadDim ? 1 : 2;
   s.tpr = threads_per_row(dim, s.NV);
   s.threads = s.tpr <= 64 ? 256 : s.tpr;
   const int rpb = s.threads / s.tpr;
-  s.grid = std::min<int64_t>(kBwdGroups, (rows + rpb - 1) / rpb);
-  s.parts = s.grid * (s.tpr <= 64 ? s.threads / 64 : 1);
+  const int resident = std::max(1, 12 / (s.threads / 64));   // workgroups of a compute unit
+  s.grid = std::min<int64_t>((int64_t)num_cus * resident, (rows + rpb - 1) / rpb);
   return s;
 }
 
 template <bool BF16, bool RBF16>
 void pick_fwd(const NormArgs& a, int NV, unsigned grid, int threads, hipStream_t st) {
-  if (a.vec) {
-    if (NV == 1) norm_fwd_kernel<BF16, RBF16, true, 1><<<grid, threads, 0, st>>>(a);
-    else norm_fwd_kernel<BF16, RBF16, true, 2><<<grid, threads, 0, st>>>(a);
-  } else {
-    if (NV == 1) norm_fwd_kernel<BF16, RBF16, false, 1><<<grid, threads, 0, st>>>(a);
-    else norm_fwd_kernel<BF16, RBF16, false, 2><<<grid, threads, 0, st>>>(a);
-  }
-}
-template <bool BF16, bool RBF16, bool VEC>
-void pick_bwd(const NormArgs& a, const BwdShape& s, hipStream_t st) {
-  const unsigned grid = (unsigned)s.grid;
-  if (s.NV == 1) norm_bwd_kernel<BF16, RBF16, VEC, 1, 512><<<grid, s.threads, 0, st>>>(a);
-  else if (s.threads <= 512) norm_bwd_kernel<BF16, RBF16, VEC, 2, 512><<<grid, s.threads, 0, st>>>(a);
-  else norm_bwd_kernel<BF16, RBF16, VEC, 2, 1024><<<grid, s.threads, 0, st>>>(a);
+  if (NV == 1) norm_fwd_kernel<BF16, RBF16, 1><<<grid, threads, 0, st>>>(a);
+  else norm_fwd_kernel<BF16, RBF16, 2><<<grid, threads, 0, st>>>(a);
 }
 template <bool BF16, bool RBF16>
 void pick_bwd(const NormArgs& a, const BwdShape& s, hipStream_t st) {
-  if (a.vec) pick_bwd<BF16, RBF16, true>(a, s, st);
-  else pick_bwd<BF16, RBF16, false>(a, s, st);
+  const unsigned grid = (unsigned)s.grid;
+  if (s.NV == 1) norm_bwd_kernel<BF16, RBF16, 1, 768, 3, BF16><<<grid, s.threads, 0, st>>>(a);
+  else if (s.threads <= 512) norm_bwd_kernel<BF16, RBF16, 2, 512, 2, false><<<grid, s.threads, 0, st>>>(a);
+  else norm_bwd_kernel<BF16, RBF16, 2, 1024, 4, false><<<grid, s.threads, 0, st>>>(a);
 }
 
 }  // namespace
 
-size_t norm_bwd_ws_bytes(int64_t rows, int64_t dim) {
-  return (size_t)bwd_shape(rows, dim).parts * 2 * (size_t)dim * sizeof(float);
+size_t norm_bwd_ws_bytes(int64_t rows, int64_t dim, int num_cus) {
+  return (size_t)bwd_shape(rows, dim, num_cus).grid * 2 * (size_t)dim * sizeof(float);
 }
 
 int launch_norm_fwd(NormArgs a, void* stream) {
@@ -494,9 +530,9 @@ int launch_norm_fwd(NormArgs a, void* stream) {
   return e == hipSuccess ? 0 : fail(6, std::string("block norm launch: ") + hipGetErrorString(e));
 }
 
-int launch_norm_bwd(NormArgs a, void* stream) {
+int launch_norm_bwd(NormArgs a, int num_cus, void* stream) {
   hipStream_t st = (hipStream_t)stream;
-  const BwdShape s = bwd_shape(a.rows, a.dim);
+  const BwdShape s = bwd_shape(a.rows, a.dim, num_cus);
   a.tpr = s.tpr;
   if (a.rows > 0) {
     if (a.act_bf16) {
@@ -508,7 +544,7 @@ int launch_norm_bwd(NormArgs a, void* stream) {
     }
   }
   if (a.dw_post != nullptr || a.dscale != nullptr || a.dw_pre != nullptr)
-    norm_sum_kernel<<<dim3((unsigned)((a.dim + 31) / 32), 2), 256, 0, st>>>(a, s.parts);
+    norm_sum_kernel<<<dim3((unsigned)((a.dim + 31) / 32), 2), 1024, 0, st>>>(a, s.grid);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? 0 : fail(6, std::string("block norm backward launch: ") + hipGetErrorString(e));
 }

@@ -6,7 +6,7 @@
 //   dw[k]  = sum_{b,t} dpre_t xx[t-(W-1)+k],    dbias = sum_{b,t} dpre_t.
 //
 // Bound by HBM: x and dout read once, dx written once (pre is recomputed).  A
-// thread takes V channels of a run of kRun tokens and slides two windows of W
+// thread takes V channels of a run of tokens and slides two windows of W
 // along it, the inputs and dpre; it starts W-1 inputs early and runs W-1 tokens
 // late, rows that its neighbours read too and that come from the caches.  dw and
 // dbias are summed in registers over the run, over a workgroup's runs by
@@ -24,7 +24,6 @@ namespace ssm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRun = 32;       // tokens of a thread's run
 constexpr int kMaxParts = 64;  // workgroups that share a channel group
 
 template <bool BF16, int V>
@@ -70,9 +69,9 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvBwdArgs a, unsig
   const int64_t nblk = a.batch * blocks_per_row;
   for (int64_t blk = part; blk < nblk; blk += a.nparts) {
     const int64_t b = blk / blocks_per_row;
-    const int64_t t0 = ((blk % blocks_per_row) * ROWS + run) * kRun;
+    const int64_t t0 = ((blk % blocks_per_row) * ROWS + run) * a.run;
     if (!active || t0 >= L) continue;
-    const int64_t t1 = min(L, t0 + kRun);
+    const int64_t t1 = min(L, t0 + a.run);
     const int64_t row0 = b * L;
     const int64_t srow = (b * dim + c0) * (W - 1);
     float xw[W][V], dp[W][V];   // xx[t-(W-1)+k]; dpre at p+j, p = t-(W-1)
@@ -171,14 +170,22 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvBwdArgs a, unsig
   }
 }
 
-// dweight and dbias from the workgroups' parts.
+// dweight and dbias from the workgroups' parts, in a fixed order: 64 sums by 4 slices of the parts.
 __global__ __launch_bounds__(256) void conv_bwd_sum_kernel(const float* ws, float* dweight, float* dbias, int64_t nparts,
                                                            int64_t dim, int width) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= dim * (width + 1)) return;
-  const int64_t k = i / dim, c = i % dim;
+  __shared__ float red[4][64];
+  const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
+  const int64_t n = dim * (width + 1), i = (int64_t)blockIdx.x * 64 + lane;
   float s = 0.f;
-  for (int64_t p = 0; p < nparts; ++p) s += ws[(p * (width + 1) + k) * dim + c];
+  if (i < n) {
+#pragma unroll 8
+    for (int64_t p = slice; p < nparts; p += 4) s += ws[p * n + i];
+  }
+  red[slice][lane] = s;
+  lds_sync();
+  if (slice != 0 || i >= n) return;
+  s = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+  const int64_t k = i / dim, c = i % dim;
   if (k < width) dweight[c * width + k] = s;
   else if (dbias != nullptr) dbias[c] = s;
 }
@@ -190,18 +197,26 @@ __global__ __launch_bounds__(256) void conv_bwd_state_kernel(const void* dstate_
   if (i < n) store1<BF16>(dstate_in, i, dstate_out != nullptr ? load1<BF16>(dstate_out, i) : 0.f);
 }
 
-int64_t blocks_of(int64_t seqlen, int V) {
-  const int rows = V == 4 ? Shape<4>::ROWS : Shape<1>::ROWS;
-  return (seqlen + (int64_t)rows * kRun - 1) / ((int64_t)rows * kRun);
-}
 int64_t groups_of(int64_t dim, int V) {
   const int64_t cw = V == 4 ? Shape<4>::COLS * 4 : Shape<1>::COLS;
   return (dim + cw - 1) / cw;
 }
+int64_t blocks_of(int64_t seqlen, int V, int run) {
+  const int rows = V == 4 ? Shape<4>::ROWS : Shape<1>::ROWS;
+  return (seqlen + (int64_t)rows * run - 1) / ((int64_t)rows * run);
+}
+// Tokens of a run: 32 (the W-1 tokens read twice are then a tenth), fewer while that leaves compute units
+// without a workgroup.
+int run_of(int64_t batch, int64_t seqlen, int64_t dim, int V, int num_cus) {
+  int run = 32;
+  while (run > 8 && batch * blocks_of(seqlen, V, run) * groups_of(dim, V) < num_cus) run /= 2;
+  return run;
+}
 // Enough workgroups for four a compute unit, as many parts at most as keep the sum of the parts short.
 int64_t parts_of(int64_t batch, int64_t seqlen, int64_t dim, int V, int num_cus) {
   const int64_t want = (4 * (int64_t)num_cus + groups_of(dim, V) - 1) / groups_of(dim, V);
-  return std::min<int64_t>(std::min<int64_t>(batch * blocks_of(seqlen, V), kMaxParts), std::max<int64_t>(want, 1));
+  const int64_t blocks = batch * blocks_of(seqlen, V, run_of(batch, seqlen, dim, V, num_cus));
+  return std::min<int64_t>(std::min<int64_t>(blocks, kMaxParts), std::max<int64_t>(want, 1));
 }
 
 template <int W>
@@ -227,7 +242,8 @@ int launch_conv_bwd(ConvBwdArgs a, int num_cus, void* stream) {
   const int V = a.vec ? 4 : 1;
   a.nparts = 0;
   if (a.seqlen > 0 && a.batch > 0) {
-    const int64_t blocks = blocks_of(a.seqlen, V), groups = groups_of(a.dim, V);
+    a.run = run_of(a.batch, a.seqlen, a.dim, V, num_cus);
+    const int64_t blocks = blocks_of(a.seqlen, V, a.run), groups = groups_of(a.dim, V);
     a.nparts = parts_of(a.batch, a.seqlen, a.dim, V, num_cus);
     if (groups * a.nparts > 0x7fffffffLL) return fail(4, "dim too large");
     const unsigned grid = (unsigned)(groups * a.nparts);
@@ -248,7 +264,7 @@ int launch_conv_bwd(ConvBwdArgs a, int num_cus, void* stream) {
     if (a.act_bf16) conv_bwd_state_kernel<true><<<(unsigned)grid, 256, 0, st>>>(a.dstate_out, a.dstate_in, n);
     else conv_bwd_state_kernel<false><<<(unsigned)grid, 256, 0, st>>>(a.dstate_out, a.dstate_in, n);
   }
-  const int64_t sums = (a.dim * (a.width + 1) + 255) / 256;
+  const int64_t sums = (a.dim * (a.width + 1) + 63) / 64;
   if (sums > 0x7fffffffLL) return fail(4, "dim too large");
   conv_bwd_sum_kernel<<<(unsigned)sums, 256, 0, st>>>(a.ws, a.dweight, a.dbias, a.nparts, a.dim, (int)a.width);
   const hipError_t e = hipGetLastError();

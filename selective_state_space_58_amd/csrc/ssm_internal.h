@@ -223,7 +223,8 @@ struct ConvBwdArgs {
   float* dbias;            // (dim) or null
   void* dstate_in;         // (batch, dim, width-1) act dtype or null
   float* ws;               // (nparts, width + 1, dim): the workgroups' shares of dweight and dbias
-  int64_t nparts;          // set by the launch
+  int64_t nparts;          // set by the launch, as is run
+  int run;                 // tokens of a thread's run
   int64_t batch, seqlen, dim, width;
   int silu;
   int act_bf16;
@@ -314,13 +315,12 @@ struct NormArgs {
   float keep_scale;         // 65536 / (65536 - drop)
   unsigned drop;            // drop probability in 65536ths
   int act_bf16, res_bf16;
-  int vec;                  // 8 columns per access
   int tpr;                  // threads of a row (set by the launch)
 };
 
-size_t norm_bwd_ws_bytes(int64_t rows, int64_t dim);
+size_t norm_bwd_ws_bytes(int64_t rows, int64_t dim, int num_cus);
 int launch_norm_fwd(NormArgs a, void* stream);
-int launch_norm_bwd(NormArgs a, void* stream);
+int launch_norm_bwd(NormArgs a, int num_cus, void* stream);
 
 int device_cu_count();
 
