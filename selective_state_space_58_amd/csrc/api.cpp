@@ -570,7 +570,7 @@ int ssm_causal_conv1d_bwd(const void* x, const float* weight, const float* bias,
   a.ws = (float*)ws;
   a.batch = batch; a.seqlen = seqlen; a.dim = dim; a.width = width; a.silu = silu;
   a.act_bf16 = act_dtype == SSM_BF16;
-  a.vec = dim % 4 == 0 && aligned(x, 4 * as) && aligned(dout, 4 * as) && aligned(dx, 4 * as);
+  a.vec = dim % 2 == 0 && aligned(x, 2 * as) && aligned(dout, 2 * as) && aligned(dx, 2 * as);
   return launch_conv_bwd(a, device_cu_count(), stream);
 }
 
@@ -591,18 +591,18 @@ static int validate_gated(const void* x, const void* r, const void* i, const flo
 
 size_t ssm_gated_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int act_dtype) {
   if (batch <= 0 || seqlen <= 0 || dim <= 0 || !elems_ok({batch, seqlen, dim})) return 0;
-  return plan_gated(batch, seqlen, dim, act_dtype == SSM_BF16, false).words_bytes;
+  return plan_gated(batch, seqlen, dim, act_dtype == SSM_BF16, dim % 2 == 0, false).words_bytes;
 }
 
 size_t ssm_gated_scan_states_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
   if (batch <= 0 || seqlen <= 0 || dim <= 0 || !elems_ok({batch, seqlen, dim})) return 0;
-  return plan_gated(batch, seqlen, dim, true, false).states_bytes;
+  return plan_gated(batch, seqlen, dim, true, true, false).states_bytes;
 }
 
 size_t ssm_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int act_dtype, int have_states) {
   if (batch <= 0 || seqlen < 0 || dim <= 0 || !elems_ok({batch, seqlen, dim})) return 0;
-  const bool bf16 = act_dtype == SSM_BF16;
-  return gated_bwd_ws_bytes(plan_gated(batch, seqlen, dim, bf16, false), plan_gated(batch, seqlen, dim, bf16, true),
+  const bool bf16 = act_dtype == SSM_BF16, vec = dim % 2 == 0;
+  return gated_bwd_ws_bytes(plan_gated(batch, seqlen, dim, bf16, vec, false), plan_gated(batch, seqlen, dim, bf16, vec, true),
                             have_states != 0);
 }
 
@@ -622,15 +622,15 @@ int ssm_gated_scan_fwd(const void* x, const void* r, const void* i, const float*
   const size_t n = (size_t)(batch * seqlen * dim) * as;
   if (overlap(y, n, x, n) || overlap(y, n, r, n) || overlap(y, n, i, n))
     return fail(SSM_ERR_SHAPE, "y must not overlap an input");
-  const GatedPlan p = plan_gated(batch, seqlen, dim, act_dtype == SSM_BF16, false);
+  const bool vec = dim % 2 == 0 && aligned(x, 2 * as) && aligned(r, 2 * as) && aligned(i, 2 * as) && aligned(y, 2 * as);
+  const GatedPlan p = plan_gated(batch, seqlen, dim, act_dtype == SSM_BF16, vec, false);
   Scratch own;
   void* ws = nullptr;
   rc = get_workspace(workspace, workspace_bytes, p.words_bytes, (hipStream_t)stream, &own, &ws);
   if (rc != SSM_OK) return rc;
   GatedArgs a{};
   a.x = x; a.r = r; a.i = i; a.A = A; a.reset = reset; a.h0 = h0; a.y = y; a.h_final = h_final; a.states = states;
-  a.batch = batch; a.seqlen = seqlen; a.dim = dim; a.form = form; a.act_bf16 = act_dtype == SSM_BF16;
-  a.vec = dim % 2 == 0 && aligned(x, 2 * as) && aligned(r, 2 * as) && aligned(i, 2 * as) && aligned(y, 2 * as);
+  a.batch = batch; a.seqlen = seqlen; a.dim = dim; a.form = form; a.act_bf16 = act_dtype == SSM_BF16; a.vec = vec;
   return launch_gated_fwd(a, p, ws, stream);
 }
 
@@ -658,7 +658,10 @@ int ssm_gated_scan_bwd(const void* x, const void* r, const void* i, const float*
     for (const void* q : in)
       if (overlap(o, n, q, n)) return fail(SSM_ERR_SHAPE, "outputs must not overlap inputs");
   const bool bf16 = act_dtype == SSM_BF16;
-  const GatedPlan fwd = plan_gated(batch, seqlen, dim, bf16, false), p = plan_gated(batch, seqlen, dim, bf16, true);
+  bool vec = dim % 2 == 0;
+  for (const void* q : in) vec = vec && aligned(q, 2 * as);
+  for (const void* o : out) vec = vec && aligned(o, 2 * as);
+  const GatedPlan fwd = plan_gated(batch, seqlen, dim, bf16, vec, false), p = plan_gated(batch, seqlen, dim, bf16, vec, true);
   Scratch own;
   void* ws = nullptr;
   rc = get_workspace(workspace, workspace_bytes, batch > 0 ? gated_bwd_ws_bytes(fwd, p, states != nullptr) : 0,
@@ -667,10 +670,7 @@ int ssm_gated_scan_bwd(const void* x, const void* r, const void* i, const float*
   GatedArgs a{};
   a.x = x; a.r = r; a.i = i; a.A = A; a.reset = reset; a.h0 = h0; a.saved = states; a.dout = dout;
   a.dh_final = dh_final; a.dx = dx; a.dr = dr; a.di = di; a.dA = dA; a.dh0 = dh0;
-  a.batch = batch; a.seqlen = seqlen; a.dim = dim; a.form = form; a.act_bf16 = act_dtype == SSM_BF16;
-  a.vec = dim % 2 == 0;
-  for (const void* q : in) a.vec = a.vec && aligned(q, 2 * as);
-  for (const void* o : out) a.vec = a.vec && aligned(o, 2 * as);
+  a.batch = batch; a.seqlen = seqlen; a.dim = dim; a.form = form; a.act_bf16 = bf16; a.vec = vec;
   return launch_gated_bwd(a, fwd, p, ws, stream);
 }
 

@@ -15,6 +15,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "ssm_internal.h"
@@ -24,28 +25,46 @@ namespace ssm {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kVec = 2;       // channels of a thread where the rows allow it
 constexpr int kMaxParts = 64;  // workgroups that share a channel group
 
+// V channels of one token as they lie in memory.
 template <bool BF16, int V>
-__device__ __forceinline__ void load_v(const void* p, int64_t i, float (&v)[V]) {
-  if constexpr (V == 4) load4<BF16>(p, i, v);
-  else v[0] = load1<BF16>(p, i);
-}
-template <bool BF16, int V>
-__device__ __forceinline__ void store_v(void* p, int64_t i, const float (&v)[V]) {
-  if constexpr (V == 4) store4<BF16>(p, i, v);
-  else store1<BF16>(p, i, v[0]);
-}
+struct Tok;
+template <>
+struct Tok<true, 2> {
+  unsigned u;
+  __device__ __forceinline__ float get(int c) const { return c == 0 ? bf16_lo(u) : bf16_hi(u); }
+  static __device__ __forceinline__ Tok make(const float (&v)[2]) { return {pack_bf16(v[0], v[1])}; }
+};
+template <>
+struct Tok<false, 2> {
+  f32x2 u;
+  __device__ __forceinline__ float get(int c) const { return u[c]; }
+  static __device__ __forceinline__ Tok make(const float (&v)[2]) { return {f32x2{v[0], v[1]}}; }
+};
+template <>
+struct Tok<true, 1> {
+  unsigned short u;
+  __device__ __forceinline__ float get(int) const { return bf16_lo(u); }
+  static __device__ __forceinline__ Tok make(const float (&v)[1]) { return {__builtin_bit_cast(unsigned short, (__bf16)v[0])}; }
+};
+template <>
+struct Tok<false, 1> {
+  float u;
+  __device__ __forceinline__ float get(int) const { return u; }
+  static __device__ __forceinline__ Tok make(const float (&v)[1]) { return {v[0]}; }
+};
 
 // A workgroup is COLS threads of V channels by ROWS runs.
 template <int V>
 struct Shape {
-  static constexpr int COLS = V == 4 ? 16 : 32;
+  static constexpr int COLS = V == 1 ? 32 : 64 / V;
   static constexpr int ROWS = kThreads / COLS;
 };
 
-template <int W, bool BF16, int V>
-__global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvBwdArgs a, unsigned groups, int64_t blocks_per_row) {
+template <int W, bool BF16, int V, bool SILU>
+__global__ __launch_bounds__(kThreads, W <= 4 ? 4 : 2) void conv_bwd_kernel(ConvBwdArgs a, unsigned groups, int64_t blocks_per_row) {
   constexpr int COLS = Shape<V>::COLS, ROWS = Shape<V>::ROWS;
   __shared__ float red[4][(W + 1) * V][COLS];
   const int64_t L = a.seqlen, dim = a.dim;
@@ -53,6 +72,8 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvBwdArgs a, unsig
   const unsigned part = blockIdx.x / groups;
   const int64_t c0 = ((int64_t)(blockIdx.x % groups) * COLS + col) * V;
   const bool active = c0 < dim;
+  using T = Tok<BF16, V>;
+  constexpr int64_t es = BF16 ? 2 : 4;
 
   float wt[W][V], bs[V], dw[W][V], db[V];
 #pragma unroll
@@ -66,84 +87,122 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvBwdArgs a, unsig
     db[c] = 0.f;
   }
 
+  constexpr int U = 4;   // tokens of a step
   const int64_t nblk = a.batch * blocks_per_row;
   for (int64_t blk = part; blk < nblk; blk += a.nparts) {
     const int64_t b = blk / blocks_per_row;
-    const int64_t t0 = ((blk % blocks_per_row) * ROWS + run) * a.run;
+    const int64_t tb = (blk % blocks_per_row) * ROWS * a.run, t0 = tb + run * a.run;
     if (!active || t0 >= L) continue;
-    const int64_t t1 = min(L, t0 + a.run);
+    const int64_t t1 = min(L, t0 + a.run), last = min(L, t1 + W - 1);   // own tokens, tokens read
     const int64_t row0 = b * L;
     const int64_t srow = (b * dim + c0) * (W - 1);
-    float xw[W][V], dp[W][V];   // xx[t-(W-1)+k]; dpre at p+j, p = t-(W-1)
+    // the workgroup's block in scalar registers, the thread's place in it in 32 bits (x, dout and dx share it)
+    const int64_t from = (row0 + tb) * dim * es;
+    const char *const x = (const char*)a.x + from, *const dy = (const char*)a.dout + from;
+    char* const dx = (char*)a.dx + from;
+    const unsigned stride = (unsigned)(dim * es);
+    unsigned off = (unsigned)((run * (int64_t)a.run * dim + c0) * es);   // of token t
+    // the inputs and dpre of a step's tokens and of the W-1 before them: xs[j] is xx[t-(W-1)+j], ds[j] dpre there
+    float xs[W - 1 + U][V], ds[W - 1 + U][V];
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
+    for (int j = 0; j < W - 1; ++j) {
+      const int64_t pos = t0 - (W - 1) + j;
 #pragma unroll
-      for (int c = 0; c < V; ++c) { xw[k][c] = 0.f; dp[k][c] = 0.f; }
-      const int64_t pos = t0 - (W - 1) + k;
-      if (k < W - 1) {
-        if (pos >= 0) {
-          load_v<BF16, V>(a.x, (row0 + pos) * dim + c0, xw[k]);
-        } else if (a.state_in != nullptr) {
+      for (int c = 0; c < V; ++c) {
+        xs[j][c] = ds[j][c] = 0.f;
+        if (pos < 0 && a.state_in != nullptr) xs[j][c] = load1<BF16>(a.state_in, srow + c * (W - 1) + (W - 1) + pos);
+      }
+      if (pos >= 0) {
+        const T v = *(const T*)(x + (off + (pos - t0) * (int64_t)stride));
 #pragma unroll
-          for (int c = 0; c < V; ++c) xw[k][c] = load1<BF16>(a.state_in, srow + c * (W - 1) + (W - 1) + pos);
-        }
+        for (int c = 0; c < V; ++c) xs[j][c] = v.get(c);
       }
     }
-#pragma unroll 4
-    for (int64_t t = t0; t < t1 + W - 1; ++t) {
-      float d[V];
+    T nx[U], nd[U];   // the next step's tokens
+    auto fetch = [&](int64_t t, unsigned off) {
 #pragma unroll
-      for (int c = 0; c < V; ++c) d[c] = 0.f;
-      if (t < L) {
-        load_v<BF16, V>(a.x, (row0 + t) * dim + c0, xw[W - 1]);
-        load_v<BF16, V>(a.dout, (row0 + t) * dim + c0, d);
-        if (a.silu) {
-#pragma unroll
-          for (int c = 0; c < V; ++c) {
-            float pre = bs[c];
-#pragma unroll
-            for (int k = 0; k < W; ++k) pre = fmaf(wt[k][c], xw[k][c], pre);
-            const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-pre * 1.4426950408889634f));
-            d[c] *= s * fmaf(pre, 1.f - s, 1.f);
-          }
+      for (int u = 0; u < U; ++u) {
+        nx[u] = {};
+        nd[u] = {};
+        if (t + u < last) {
+          nx[u] = *(const T*)(x + (off + u * stride));
+          nd[u] = *(const T*)(dy + (off + u * stride));
         }
-        if (t < t1) {
+      }
+    };
+    // EDGE: the step reaches out of the run's own tokens
+    auto step = [&](int64_t t, auto edge) {
+      constexpr bool EDGE = decltype(edge)::value;
 #pragma unroll
-          for (int c = 0; c < V; ++c) {
-            db[c] += d[c];
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int k = 0; k < W; ++k) dw[k][c] = fmaf(d[c], xw[k][c], dw[k][c]);
-          }
+        for (int c = 0; c < V; ++c) {
+          xs[W - 1 + u][c] = nx[u].get(c);
+          ds[W - 1 + u][c] = nd[u].get(c);   // zeros behind the last token
+        }
+      if (EDGE || t + 2 * U > last) {
+        fetch(t + U, off + U * stride);
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          nx[u] = *(const T*)(x + (off + (U + u) * stride));
+          nd[u] = *(const T*)(dy + (off + (U + u) * stride));
         }
       }
 #pragma unroll
-      for (int j = 0; j < W - 1; ++j)
+      for (int u = 0; u < U; ++u) {
+        const bool own = !EDGE || t + u < t1;
+        if (EDGE && t + u >= last) {
 #pragma unroll
-        for (int c = 0; c < V; ++c) { dp[j][c] = dp[j + 1][c]; xw[j][c] = xw[j + 1][c]; }
+          for (int c = 0; c < V; ++c) ds[W - 1 + u][c] = 0.f;
+        }
 #pragma unroll
-      for (int c = 0; c < V; ++c) dp[W - 1][c] = d[c];
-      const int64_t p = t - (W - 1);
-      if (p >= t0 || t0 == 0) {
+        for (int c = 0; c < V; ++c) {
+          float& d = ds[W - 1 + u][c];
+          if constexpr (SILU) {
+            float pre = bs[c];
+#pragma unroll
+            for (int k = 0; k < W; ++k) pre = fmaf(wt[k][c], xs[u + k][c], pre);
+            const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-pre * 1.4426950408889634f));
+            d *= s * fmaf(pre, 1.f - s, 1.f);
+          }
+          if (own) {
+            db[c] += d;
+#pragma unroll
+            for (int k = 0; k < W; ++k) dw[k][c] = fmaf(d, xs[u + k][c], dw[k][c]);
+          }
+        }
+        const int64_t p = t + u - (W - 1);
+        if (EDGE && (p >= t1 || (p < t0 && t0 > 0))) continue;   // another run's
         float o[V];
 #pragma unroll
         for (int c = 0; c < V; ++c) {
           o[c] = 0.f;
 #pragma unroll
-          for (int j = 0; j < W; ++j) o[c] = fmaf(wt[W - 1 - j][c], dp[j][c], o[c]);
+          for (int j = 0; j < W; ++j) o[c] = fmaf(wt[W - 1 - j][c], ds[u + j][c], o[c]);
         }
-        const int64_t q = p - L + (W - 1);   // place in the carried-out state
-        if (a.dstate_out != nullptr && q >= 0) {
+        if (EDGE && a.dstate_out != nullptr && p - L + (W - 1) >= 0) {   // one of the segment's last inputs
 #pragma unroll
-          for (int c = 0; c < V; ++c) o[c] += load1<BF16>(a.dstate_out, srow + c * (W - 1) + q);
+          for (int c = 0; c < V; ++c) o[c] += load1<BF16>(a.dstate_out, srow + c * (W - 1) + p - L + (W - 1));
         }
-        if (p >= 0) {
-          store_v<BF16, V>(a.dx, (row0 + p) * dim + c0, o);
+        if (!EDGE || p >= 0) {
+          *(T*)(dx + (EDGE ? off + (u - (W - 1)) * (int64_t)stride : off + (u - (W - 1)) * stride)) = T::make(o);
         } else if (a.dstate_in != nullptr) {
 #pragma unroll
           for (int c = 0; c < V; ++c) store1<BF16>(a.dstate_in, srow + c * (W - 1) + (W - 1) + p, o[c]);
         }
       }
-    }
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int c = 0; c < V; ++c) { xs[j][c] = xs[j + U][c]; ds[j][c] = ds[j + U][c]; }
+      off += U * stride;
+    };
+    fetch(t0, off);
+    int64_t t = t0;
+    for (; t < t0 + W - 1; t += U) step(t, std::true_type{});
+    for (; t + U <= t1; t += U) step(t, std::false_type{});
+    for (; t < t1 + W - 1; t += U) step(t, std::true_type{});
   }
 
   // runs of the wave, then the waves
@@ -198,11 +257,11 @@ __global__ __launch_bounds__(256) void conv_bwd_state_kernel(const void* dstate_
 }
 
 int64_t groups_of(int64_t dim, int V) {
-  const int64_t cw = V == 4 ? Shape<4>::COLS * 4 : Shape<1>::COLS;
+  const int64_t cw = V == 1 ? Shape<1>::COLS : Shape<kVec>::COLS * kVec;
   return (dim + cw - 1) / cw;
 }
 int64_t blocks_of(int64_t seqlen, int V, int run) {
-  const int rows = V == 4 ? Shape<4>::ROWS : Shape<1>::ROWS;
+  const int rows = V == 1 ? Shape<1>::ROWS : Shape<kVec>::ROWS;
   return (seqlen + (int64_t)rows * run - 1) / ((int64_t)rows * run);
 }
 // Tokens of a run: 32 (the W-1 tokens read twice are then a tenth), fewer while that leaves compute units
@@ -212,40 +271,44 @@ int run_of(int64_t batch, int64_t seqlen, int64_t dim, int V, int num_cus) {
   while (run > 8 && batch * blocks_of(seqlen, V, run) * groups_of(dim, V) < num_cus) run /= 2;
   return run;
 }
-// Enough workgroups for four a compute unit, as many parts at most as keep the sum of the parts short.
+// Workgroups that share a channel group: about four a compute unit in all, each with as many blocks as the
+// others (64 blocks by 43 workgroups left a third of them idle half the time: 36.6 us against 33 by 32), and few
+// enough to keep the sum of the parts short.
 int64_t parts_of(int64_t batch, int64_t seqlen, int64_t dim, int V, int num_cus) {
-  const int64_t want = (4 * (int64_t)num_cus + groups_of(dim, V) - 1) / groups_of(dim, V);
+  const int64_t want = std::min<int64_t>(kMaxParts, std::max<int64_t>(1, 4 * (int64_t)num_cus / groups_of(dim, V)));
   const int64_t blocks = batch * blocks_of(seqlen, V, run_of(batch, seqlen, dim, V, num_cus));
-  return std::min<int64_t>(std::min<int64_t>(blocks, kMaxParts), std::max<int64_t>(want, 1));
+  const int64_t each = std::max<int64_t>(1, (blocks + want - 1) / want);
+  return (blocks + each - 1) / each;
 }
 
+template <int W, bool BF16, int V>
+void launch(const ConvBwdArgs& a, unsigned grid, unsigned groups, int64_t blocks, hipStream_t st) {
+  if (a.silu) conv_bwd_kernel<W, BF16, V, true><<<grid, kThreads, 0, st>>>(a, groups, blocks);
+  else conv_bwd_kernel<W, BF16, V, false><<<grid, kThreads, 0, st>>>(a, groups, blocks);
+}
 template <int W>
 void launch_w(const ConvBwdArgs& a, unsigned grid, unsigned groups, int64_t blocks, hipStream_t st) {
-  if (a.vec) {
-    if (a.act_bf16) conv_bwd_kernel<W, true, 4><<<grid, kThreads, 0, st>>>(a, groups, blocks);
-    else conv_bwd_kernel<W, false, 4><<<grid, kThreads, 0, st>>>(a, groups, blocks);
-  } else {
-    if (a.act_bf16) conv_bwd_kernel<W, true, 1><<<grid, kThreads, 0, st>>>(a, groups, blocks);
-    else conv_bwd_kernel<W, false, 1><<<grid, kThreads, 0, st>>>(a, groups, blocks);
-  }
+  if (a.vec) a.act_bf16 ? launch<W, true, kVec>(a, grid, groups, blocks, st) : launch<W, false, kVec>(a, grid, groups, blocks, st);
+  else a.act_bf16 ? launch<W, true, 1>(a, grid, groups, blocks, st) : launch<W, false, 1>(a, grid, groups, blocks, st);
 }
 
 }  // namespace
 
 size_t conv_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int num_cus) {
-  const int64_t parts = std::max(parts_of(batch, seqlen, dim, 1, num_cus), parts_of(batch, seqlen, dim, 4, num_cus));
+  const int64_t parts = std::max(parts_of(batch, seqlen, dim, 1, num_cus), parts_of(batch, seqlen, dim, kVec, num_cus));
   return (size_t)parts * (size_t)(width + 1) * (size_t)dim * sizeof(float);
 }
 
 int launch_conv_bwd(ConvBwdArgs a, int num_cus, void* stream) {
   hipStream_t st = (hipStream_t)stream;
-  const int V = a.vec ? 4 : 1;
+  const int V = a.vec ? kVec : 1;
   a.nparts = 0;
   if (a.seqlen > 0 && a.batch > 0) {
     a.run = run_of(a.batch, a.seqlen, a.dim, V, num_cus);
     const int64_t blocks = blocks_of(a.seqlen, V, a.run), groups = groups_of(a.dim, V);
     a.nparts = parts_of(a.batch, a.seqlen, a.dim, V, num_cus);
-    if (groups * a.nparts > 0x7fffffffLL) return fail(4, "dim too large");
+    // (a thread's place in its workgroup's block is held in 32 bits)
+    if (groups * a.nparts > 0x7fffffffLL || a.dim > 0x7fffffffLL / (4 * 1024)) return fail(4, "dim too large");
     const unsigned grid = (unsigned)(groups * a.nparts);
     switch (a.width) {
       case 1: launch_w<1>(a, grid, (unsigned)groups, blocks, st); break;

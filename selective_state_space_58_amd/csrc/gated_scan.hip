@@ -434,6 +434,8 @@ __global__ __launch_bounds__(64 * NW, 4) void gated_fwd_kernel(GatedArgs a) {
 // Hides where a value comes from, so that what is formed from it again is
 // formed again and not kept in registers from the first time.
 __device__ __forceinline__ void forget(float& v) { asm("" : "+v"(v)); }
+// Keeps a value where it is formed: put off to its use, what it is formed from would stay in registers.
+__device__ __forceinline__ void keep_here(float& v) { asm volatile("" : "+v"(v)); }
 template <int V>
 __device__ __forceinline__ void forget(Raw<true, V>& r) { asm("" : "+v"(r.u)); }
 template <int V>
@@ -576,6 +578,7 @@ __global__ __launch_bounds__(64 * NW, 4) void gated_bwd_kernel(GatedArgs a) {
         for (int v = 0; v < V; ++v) {
           const float b = hp[j][v];
           hp[j][v] = st[v];
+          keep_here(hp[j][v]);
           st[v] = rs ? b : fmaf(da[j][v], st[v], b);
         }
       }
@@ -670,10 +673,9 @@ __global__ __launch_bounds__(64 * NW, 4) void gated_bwd_kernel(GatedArgs a) {
 
 // Clears the published words and the counter of a pass.
 __global__ __launch_bounds__(256) void gated_clear_kernel(uint64_t* words, int64_t n, unsigned* count) {
-  const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
+  const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;   // n is even, words 256-byte aligned
   if (k == 0) *count = 0;
-  if (k < n) words[k] = ~0ull;
-  if (k + 1 < n) words[k + 1] = ~0ull;
+  if (k < n) *reinterpret_cast<u32x4*>(words + k) = u32x4{~0u, ~0u, ~0u, ~0u};
 }
 
 // dA[d] = sum of the parts (tile, batch) of channel d, in a fixed order: 32
@@ -684,6 +686,7 @@ __global__ __launch_bounds__(1024) void gated_da_kernel(const float* parts, floa
   const int64_t c = (int64_t)blockIdx.x * 32 + col;
   float s = 0.f;
   if (c < dim)
+#pragma unroll 8
     for (int64_t k = slice; k < n; k += 32) s += parts[k * dim + c];
   red[slice][col] = s;
   lds_sync();
@@ -718,14 +721,14 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedArgs a) {
 }
 
 // Tokens of a lane's run: what four waves a SIMD leave registers for.
-constexpr int run_len(bool bf16, bool bwd) { return (bf16 ? 16 : 8) / (bwd ? 2 : 1); }
+constexpr int run_len(bool bf16, int V, bool bwd) { return (bf16 || V == 1 ? 16 : 8) / (bwd ? 2 : 1); }
 
 // Instances: V = 2 where the rows allow it, with and without resets; the
 // one-channel kernels always look for them.
 template <bool BF16, int V, int FORM, bool RESET>
 void launch(const GatedArgs& a, unsigned grid, bool bwd, hipStream_t st) {
-  if (bwd) gated_bwd_kernel<BF16, V, FORM, RESET, run_len(BF16, true)><<<grid, 64 * NW, 0, st>>>(a);
-  else gated_fwd_kernel<BF16, V, FORM, RESET, run_len(BF16, false)><<<grid, 64 * NW, 0, st>>>(a);
+  if (bwd) gated_bwd_kernel<BF16, V, FORM, RESET, run_len(BF16, V, true)><<<grid, 64 * NW, 0, st>>>(a);
+  else gated_fwd_kernel<BF16, V, FORM, RESET, run_len(BF16, V, false)><<<grid, 64 * NW, 0, st>>>(a);
 }
 template <bool BF16, int FORM>
 void pick(const GatedArgs& a, unsigned grid, bool bwd, hipStream_t st) {
@@ -746,13 +749,14 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
 // Columns: as many lanes across the channels as there are channels for, up to 32 (a 128-byte row of bf16
-// pairs); the other lanes go along time.
-GatedPlan plan_gated(int64_t batch, int64_t seqlen, int64_t dim, bool bf16, bool bwd) {
+// pairs); the other lanes go along time.  vec: two channels a lane, for even dim only; an even dim without it
+// has tiles at least as long, so the workspace of the one is enough for the other.
+GatedPlan plan_gated(int64_t batch, int64_t seqlen, int64_t dim, bool bf16, bool vec, bool bwd) {
   GatedPlan p{4, 0, 1, 0, 0, 0};
   if (batch == 0 || dim == 0) return p;
   const int V = dim % 2 == 0 ? 2 : 1;
   while (p.cols < kGatedMaxCols && (int64_t)p.cols * V < dim) p.cols *= 2;
-  p.tile = (int64_t)NW * (64 / p.cols) * run_len(bf16, bwd);
+  p.tile = (int64_t)NW * (64 / p.cols) * run_len(bf16, vec ? 2 : 1, bwd);
   p.ntiles = std::max<int64_t>(1, (seqlen + p.tile - 1) / p.tile);
   const size_t plane = (size_t)(batch * dim);
   p.words_bytes = p.ntiles > 1 ? up256(2 * p.ntiles * plane * sizeof(uint64_t)) + 256 : 0;

@@ -228,7 +228,7 @@ struct ConvBwdArgs {
   int64_t batch, seqlen, dim, width;
   int silu;
   int act_bf16;
-  int vec;                 // 4 channels per thread with 8/16-byte accesses
+  int vec;                 // two channels per thread
 };
 
 size_t conv_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t width, int num_cus);
@@ -276,7 +276,7 @@ struct GatedPlan {
   int64_t tile, ntiles;        // tokens of a tile
   size_t words_bytes, da_bytes, states_bytes;
 };
-GatedPlan plan_gated(int64_t batch, int64_t seqlen, int64_t dim, bool bf16, bool bwd);
+GatedPlan plan_gated(int64_t batch, int64_t seqlen, int64_t dim, bool bf16, bool vec, bool bwd);
 // ws: words_bytes of the plan
 int launch_gated_fwd(GatedArgs a, const GatedPlan& p, void* ws, void* stream);
 // ws: gated_bwd_ws_bytes; fwd: the forward's plan, for the states where a.saved is null

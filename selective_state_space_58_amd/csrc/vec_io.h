@@ -33,46 +33,4 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
   else ((float*)p)[i] = v;
 }
 
-// Four values.
-template <bool BF16>
-__device__ __forceinline__ void load4(const void* p, int64_t i, float (&v)[4]) {
-  if (BF16) {
-    const u32x2 r = *reinterpret_cast<const u32x2*>((const unsigned short*)p + i);
-    v[0] = bf16_lo(r[0]); v[1] = bf16_hi(r[0]); v[2] = bf16_lo(r[1]); v[3] = bf16_hi(r[1]);
-  } else {
-    const f32x4 r = *reinterpret_cast<const f32x4*>((const float*)p + i);
-    v[0] = r[0]; v[1] = r[1]; v[2] = r[2]; v[3] = r[3];
-  }
-}
-template <bool BF16>
-__device__ __forceinline__ void store4(void* p, int64_t i, const float (&v)[4]) {
-  if (BF16) *reinterpret_cast<u32x2*>((unsigned short*)p + i) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-  else *reinterpret_cast<f32x4*>((float*)p + i) = f32x4{v[0], v[1], v[2], v[3]};
-}
-
-// Eight values (fp32: two 16-byte accesses).
-template <bool BF16>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
-  if (BF16) {
-    const u32x4 r = *reinterpret_cast<const u32x4*>((const unsigned short*)p + i);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) { v[2 * q] = bf16_lo(r[q]); v[2 * q + 1] = bf16_hi(r[q]); }
-  } else {
-    const f32x4 r = *reinterpret_cast<const f32x4*>((const float*)p + i);
-    const f32x4 s = *reinterpret_cast<const f32x4*>((const float*)p + i + 4);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) { v[q] = r[q]; v[q + 4] = s[q]; }
-  }
-}
-template <bool BF16>
-__device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
-  if (BF16) {
-    *reinterpret_cast<u32x4*>((unsigned short*)p + i) =
-        u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
-  } else {
-    *reinterpret_cast<f32x4*>((float*)p + i) = f32x4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4*>((float*)p + i + 4) = f32x4{v[4], v[5], v[6], v[7]};
-  }
-}
-
 }  // namespace ssm
