@@ -87,44 +87,56 @@ struct Cols {
   __device__ __forceinline__ int at(int j) const { return (j * tpr + tid) * 8; }
   __device__ __forceinline__ int n(int j) const { return dim - at(j); }
 };
+// A whole pack at element `i`, and one of which only n < 8 elements exist.
 template <bool BF16>
-__device__ __forceinline__ Pack<BF16> load_raw(const void* p, int64_t row, const Cols& c, int j) {
-  Pack<BF16> r = {};
-  const char* q = (const char*)p + (row + c.at(j)) * (BF16 ? 2 : 4);
-  if (c.n(j) >= 8) {
-    r.u[0] = *reinterpret_cast<const u32x4_any*>(q);
-    if (!BF16) r.u[BF16 ? 0 : 1] = *reinterpret_cast<const u32x4_any*>(q + 16);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 7; ++e)
-      if (e < c.n(j)) {
-        if (BF16) r.u[0][e / 2] |= (unsigned)((const unsigned short*)q)[e] << (16 * (e % 2));
-        else r.u[BF16 ? 0 : e / 4][e % 4] = ((const unsigned*)q)[e];
-      }
-  }
+__device__ __forceinline__ Pack<BF16> load_whole(const void* p, int64_t i) {
+  const char* q = (const char*)p + i * (BF16 ? 2 : 4);
+  Pack<BF16> r;
+  r.u[0] = *reinterpret_cast<const u32x4_any*>(q);
+  if (!BF16) r.u[BF16 ? 0 : 1] = *reinterpret_cast<const u32x4_any*>(q + 16);
   return r;
 }
 template <bool BF16>
+__device__ __forceinline__ Pack<BF16> load_part(const void* p, int64_t i, int n) {
+  Pack<BF16> r = {};
+#pragma unroll
+  for (int e = 0; e < 7; ++e)
+    if (e < n) {
+      if (BF16) r.u[0][e / 2] |= (unsigned)((const unsigned short*)p)[i + e] << (16 * (e % 2));
+      else r.u[BF16 ? 0 : e / 4][e % 4] = ((const unsigned*)p)[i + e];
+    }
+  return r;
+}
+// NT: a store that is not kept in the caches.
+template <bool BF16, bool NT>
+__device__ __forceinline__ void store_whole(void* p, int64_t i, const Pack<BF16>& r) {
+  u32x4_any* q = reinterpret_cast<u32x4_any*>((char*)p + i * (BF16 ? 2 : 4));
+#pragma unroll
+  for (int k = 0; k < (BF16 ? 1 : 2); ++k) {
+    if (NT) __builtin_nontemporal_store(r.u[k], q + k);
+    else q[k] = r.u[k];
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void store_part(void* p, int64_t i, int n, const Pack<BF16>& r) {
+#pragma unroll
+  for (int e = 0; e < 7; ++e)
+    if (e < n) {
+      if (BF16) ((unsigned short*)p)[i + e] = (unsigned short)(r.u[0][e / 2] >> (16 * (e % 2)));
+      else ((unsigned*)p)[i + e] = r.u[BF16 ? 0 : e / 4][e % 4];
+    }
+}
+template <bool BF16>
 __device__ __forceinline__ void load_pack(const void* p, int64_t row, const Cols& c, int j, float (&v)[8]) {
-  const Pack<BF16> r = load_raw<BF16>(p, row, c, j);
+  const Pack<BF16> r = c.n(j) >= 8 ? load_whole<BF16>(p, row + c.at(j)) : load_part<BF16>(p, row + c.at(j), c.n(j));
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = r.get(e);
 }
-template <bool BF16>
+template <bool BF16, bool NT>
 __device__ __forceinline__ void store_pack(void* p, int64_t row, const Cols& c, int j, const float (&v)[8]) {
   const Pack<BF16> r = Pack<BF16>::make(v);
-  char* q = (char*)p + (row + c.at(j)) * (BF16 ? 2 : 4);
-  if (c.n(j) >= 8) {
-    *reinterpret_cast<u32x4_any*>(q) = r.u[0];
-    if (!BF16) *reinterpret_cast<u32x4_any*>(q + 16) = r.u[BF16 ? 0 : 1];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 7; ++e)
-      if (e < c.n(j)) {
-        if (BF16) ((unsigned short*)q)[e] = (unsigned short)(r.u[0][e / 2] >> (16 * (e % 2)));
-        else ((unsigned*)q)[e] = r.u[BF16 ? 0 : e / 4][e % 4];
-      }
-  }
+  if (c.n(j) >= 8) store_whole<BF16, NT>(p, row + c.at(j), r);
+  else store_part<BF16>(p, row + c.at(j), c.n(j), r);
 }
 // Keep bits of a pack; in rows that do not start at a whole block it lies in two of them.
 __device__ __forceinline__ unsigned keep_pack(const NormArgs& a, int64_t row, const Cols& c, int j) {
@@ -135,15 +147,38 @@ __device__ __forceinline__ unsigned keep_pack(const NormArgs& a, int64_t row, co
   return m;
 }
 
-// Sums N values over the threads of a row, the same order for every thread.
-// Rows within a wave: shuffles.  Rows of several waves: shuffles, then LDS in the
-// order of the waves (every wave of the workgroup makes the same calls).
+// The lane's value of a permutation within 16 lanes, as an operand.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+// Sum over the 8, 16, 32 or 64 lanes that share a row, in every one of them: pairs, quads, then mirrored halves of
+// 8 and 16 lanes (one instruction each), then rows of 16 and halves of the wave swapped.
+__device__ __forceinline__ float lane_sum(float v, int lanes) {
+  v += dpp<0xB1>(v);    // lane ^ 1
+  v += dpp<0x4E>(v);    // lane ^ 2
+  v += dpp<0x141>(v);   // 7 - lane of 8
+  if (lanes >= 16) v += dpp<0x140>(v);   // 15 - lane of 16
+  if (lanes >= 32) {
+    const unsigned u = __builtin_bit_cast(unsigned, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    v = __builtin_bit_cast(float, (unsigned)r[0]) + __builtin_bit_cast(float, (unsigned)r[1]);
+  }
+  if (lanes >= 64) {
+    const unsigned u = __builtin_bit_cast(unsigned, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    v = __builtin_bit_cast(float, (unsigned)r[0]) + __builtin_bit_cast(float, (unsigned)r[1]);
+  }
+  return v;
+}
+
+// Sums N values over the threads of a row, the same order for every thread:
+// over lanes, and for rows of several waves through LDS in the order of the waves
+// (every wave of the workgroup makes the same calls).
 template <int N>
 __device__ __forceinline__ void row_sum(float (&s)[N], int tpr, float (*red)[N], int& buf) {
-  const int top = tpr < 64 ? tpr : 64;
-  for (int sh = 1; sh < top; sh <<= 1)
 #pragma unroll
-    for (int n = 0; n < N; ++n) s[n] += __shfl_xor(s[n], sh);
+  for (int n = 0; n < N; ++n) s[n] = lane_sum(s[n], tpr);
   if (tpr > 64) {
     const int waves = tpr / 64, wave = threadIdx.x >> 6;
     float(*r)[N] = red + buf * kMaxWaves;
@@ -154,6 +189,7 @@ __device__ __forceinline__ void row_sum(float (&s)[N], int tpr, float (*red)[N],
     lds_sync();
 #pragma unroll
     for (int n = 0; n < N; ++n) s[n] = 0.f;
+#pragma unroll 4
     for (int w = 0; w < waves; ++w)
 #pragma unroll
       for (int n = 0; n < N; ++n) s[n] += r[w][n];
@@ -215,7 +251,7 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[j][e] += q[e];
     }
-    if (a.res_out != nullptr) store_pack<RBF16>(a.res_out, row, c, j, v[j]);
+    if (a.res_out != nullptr) store_pack<RBF16, true>(a.res_out, row, c, j, v[j]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[0] = fmaf(v[j][e], v[j][e], s[0]);
   }
@@ -228,18 +264,22 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a) {
       load_pack<false>(a.w_pre, 0, c, j, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] *= v[j][e] * r2;
-      store_pack<BF16>(a.out, row, c, j, w);
+      store_pack<BF16, true>(a.out, row, c, j, w);
     }
   }
 }
 
-// Gradient.  With vhat = v / rms(v), Rhat = R / rms(R), q = dout w_pre, w = w_post scale:
-//   dR = dres + (q - Rhat mean(q Rhat)) / rms(R),  dm = dropout(dR),  dn = w dm
-//   dv = (dn - vhat mean(dn vhat)) / rms(v)
-//   dw_post = scale S, dscale = w_post S with S = sum_rows dm vhat;  dw_pre = sum_rows dout Rhat
+// Gradient.  With r1 = 1 / rms(v), r2 = 1 / rms(R), w = w_post scale, m = dropout(w r1 v), q = dout w_pre:
+//   dR = dres + r2 q - k2 R,       k2 = r2^3 mean(q R)
+//   dm = dropout(dR),  dv = r1 (w dm - k1 v),   k1 = r1^2 mean(w dm v) = r1 mean(m dR)
+//   dw_post = scale S, dscale = w_post S with S = sum_rows dm r1 v;  dw_pre = sum_rows dout r2 R
+// (dropout is diagonal, so it moves from dR to m), and mean(m dR) is mean(m dres) + r2 mean(m q) - k2 mean(m R):
+// two rounds of sums over a row, sum v^2 and then five at once.
 // A workgroup walks rows that lie gridDim.x apart and keeps its share of S and
-// dw_pre in registers.  AHEAD: the next row's loads are issued before the present
-// row's sums, whose three rounds of waiting they fill.
+// dw_pre in registers.  LEAN, for rows that leave a thread 128 registers for two
+// packs: the weights are read again where they are used, and v and R formed again
+// for the gradients.  (The next row's loads ahead of the sums: no gain where the
+// packs' loads stand in one branch, 425 against 422 us on 16384 x 5120.)
 template <bool BF16, bool RBF16, int NV>
 struct Row {
   Pack<BF16> y[NV], z[NV], dout[NV];
@@ -247,72 +287,77 @@ struct Row {
   __device__ __forceinline__ void load(const NormArgs& a, int64_t row, const Cols& c) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      y[j] = load_raw<BF16>(a.y, row, c, j);
-      if (a.z != nullptr) z[j] = load_raw<BF16>(a.z, row, c, j);
-      if (a.w_pre != nullptr) {
-        if (a.residual != nullptr) res[j] = load_raw<RBF16>(a.residual, row, c, j);
-        dout[j] = load_raw<BF16>(a.dout, row, c, j);
+      const int64_t i = row + c.at(j);
+      const int n = c.n(j);
+      if (n >= 8) {
+        y[j] = load_whole<BF16>(a.y, i);
+        if (a.z != nullptr) z[j] = load_whole<BF16>(a.z, i);
+        if (a.w_pre != nullptr) dout[j] = load_whole<BF16>(a.dout, i);
+        if (a.w_pre != nullptr && a.residual != nullptr) res[j] = load_whole<RBF16>(a.residual, i);
+        if (a.dres != nullptr) dres[j] = load_whole<RBF16>(a.dres, i);
+      } else {
+        y[j] = load_part<BF16>(a.y, i, n);
+        if (a.z != nullptr) z[j] = load_part<BF16>(a.z, i, n);
+        if (a.w_pre != nullptr) dout[j] = load_part<BF16>(a.dout, i, n);
+        if (a.w_pre != nullptr && a.residual != nullptr) res[j] = load_part<RBF16>(a.residual, i, n);
+        if (a.dres != nullptr) dres[j] = load_part<RBF16>(a.dres, i, n);
       }
-      if (a.dres != nullptr) dres[j] = load_raw<RBF16>(a.dres, row, c, j);
     }
   }
 };
 // Hides that a pack was unpacked before, so that it is kept packed and unpacked again.
 template <bool BF16>
 __device__ __forceinline__ void forget(Pack<BF16>& p) {
-  if (BF16) asm("" : "+v"(p.u[0]));
+#pragma unroll
+  for (int k = 0; k < (BF16 ? 1 : 2); ++k) asm("" : "+v"(p.u[k]));
 }
 
-template <bool BF16, bool RBF16, int NV, int MAXT, int WAVES, bool AHEAD>
+template <bool BF16, bool RBF16, int NV, int MAXT, int WAVES, bool LEAN>
 __global__ __launch_bounds__(MAXT, WAVES) void norm_bwd_kernel(NormArgs a) {
   __shared__ float red1[2 * kMaxWaves][1];
-  __shared__ float red2[2 * kMaxWaves][2];
+  __shared__ float red2[2 * kMaxWaves][5];
   const int rpb = blockDim.x / a.tpr;
   const int tid = threadIdx.x % a.tpr;
   const float inv = 1.f / (float)a.dim;
   int buf1 = 0, buf2 = 0;
-  float gs[NV][8], gpre[NV][8], w[NV][8], wpre[NV][8];
-  {
+  float gs[NV][8], gpre[NV][8];
+  // w and w_pre of a thread's pack j
+  auto weights = [&](int j, float (&w)[8], float (&wpre)[8]) {
     const Cols c{tid, a.tpr, (int)a.dim};
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        gs[j][e] = gpre[j][e] = wpre[j][e] = 0.f;
-        w[j][e] = 1.f;
-      }
-      if (a.w_post != nullptr) load_pack<false>(a.w_post, 0, c, j, w[j]);
-      if (a.scale != nullptr) {
-        float sc[8];
-        load_pack<false>(a.scale, 0, c, j, sc);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[j][e] *= sc[e];
-      }
-      if (a.w_pre != nullptr) load_pack<false>(a.w_pre, 0, c, j, wpre[j]);
+    for (int e = 0; e < 8; ++e) {
+      wpre[e] = 0.f;
+      w[e] = 1.f;
     }
+    if (a.w_post != nullptr) load_pack<false>(a.w_post, 0, c, j, w);
+    if (a.scale != nullptr) {
+      float sc[8];
+      load_pack<false>(a.scale, 0, c, j, sc);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] *= sc[e];
+    }
+    if (a.w_pre != nullptr) load_pack<false>(a.w_pre, 0, c, j, wpre);
+  };
+  float w[NV][8], wpre[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) gs[j][e] = gpre[j][e] = 0.f;
+    if (!LEAN) weights(j, w[j], wpre[j]);
   }
 
   const int64_t stride = (int64_t)gridDim.x * rpb;
   int64_t r = (int64_t)blockIdx.x * rpb + threadIdx.x / a.tpr;
   auto cols_of = [&](int64_t r) { return Cols{tid, a.tpr, r < a.rows ? (int)a.dim : 0}; };
-  Row<BF16, RBF16, NV> next = {};
-  if (AHEAD) next.load(a, r < a.rows ? r * a.dim : 0, cols_of(r));
-  // (a workgroup's rows are walked together: the sums meet at barriers)
-  for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < a.rows; r0 += stride, r += stride) {
+  auto start = [&](int64_t r) { return r < a.rows ? r * a.dim : 0; };
+  // one row a thread of the workgroup's, from its packs
+  auto row_of = [&](int64_t r, Row<BF16, RBF16, NV>& q) {
     const Cols c = cols_of(r);
-    const int64_t row = r < a.rows ? r * a.dim : 0;
-    Row<BF16, RBF16, NV> q = {};
-    if (AHEAD) {
-      q = next;
-      if (r0 + stride < a.rows) next.load(a, r + stride < a.rows ? (r + stride) * a.dim : 0, cols_of(r + stride));
-    } else {
-      q.load(a, row, c);
-    }
-    float v[NV][8], R[NV][8];   // R: then dn
+    const int64_t row = start(r);
+    float v[NV][8], R[NV][8];
     unsigned keep[NV];
     float s1[1] = {0.f};
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
+    auto branch = [&](int j) {   // v
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         v[j][e] = q.y[j].get(e);
@@ -320,8 +365,13 @@ __global__ __launch_bounds__(MAXT, WAVES) void norm_bwd_kernel(NormArgs a) {
           const float zz = q.z[j].get(e);
           v[j][e] *= zz * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-zz * kLog2e));
         }
-        s1[0] = fmaf(v[j][e], v[j][e], s1[0]);
       }
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      branch(j);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s1[0] = fmaf(v[j][e], v[j][e], s1[0]);
       keep[j] = a.drop != 0 ? keep_pack(a, row, c, j) : 0xffu;
     }
     float r1 = 1.f;
@@ -330,58 +380,63 @@ __global__ __launch_bounds__(MAXT, WAVES) void norm_bwd_kernel(NormArgs a) {
       r1 = __builtin_amdgcn_rsqf(fmaf(s1[0], inv, a.eps));
     }
     const float rk = r1 * a.keep_scale;
-    float r2 = 0.f, k2 = 0.f;
-    if (a.w_pre != nullptr) {   // R, and with it sum R^2 and sum q R
-      float s2[2] = {0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          R[j][e] = q.res[j].get(e) + ((keep[j] >> e) & 1u ? v[j][e] * rk * w[j][e] : 0.f);
-          s2[0] = fmaf(R[j][e], R[j][e], s2[0]);
-          s2[1] = fmaf(R[j][e], q.dout[j].get(e) * wpre[j][e], s2[1]);
-        }
-      row_sum<2>(s2, a.tpr, red2, buf2);
-      r2 = __builtin_amdgcn_rsqf(fmaf(s2[0], inv, a.eps));
-      k2 = s2[1] * inv * r2 * r2;
-    } else {
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) R[j][e] = 0.f;
-    }
-    float s3[1] = {0.f};
+    auto again = [&](int j) {   // LEAN: what the other forms keep
+      if (!LEAN) return;
+      forget(q.y[j]);
+      forget(q.z[j]);
+      forget(q.res[j]);
+      branch(j);
+      weights(j, w[j], wpre[j]);
+    };
+    // m, and R where it is asked for
+    auto scaled = [&](int j, int e) { return (keep[j] >> e) & 1u ? v[j][e] * rk * w[j][e] : 0.f; };
+    float s[5] = {0.f, 0.f, 0.f, 0.f, 0.f};   // R^2, q R, m dres, m q, m R
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      float dR[8];
+      again(j);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float m = scaled(j, e);
+        s[2] = fmaf(m, q.dres[j].get(e), s[2]);
+        R[j][e] = 0.f;
+        if (a.w_pre != nullptr) {
+          R[j][e] = q.res[j].get(e) + m;
+          const float d = q.dout[j].get(e) * wpre[j][e];
+          s[0] = fmaf(R[j][e], R[j][e], s[0]);
+          s[1] = fmaf(R[j][e], d, s[1]);
+          s[3] = fmaf(m, d, s[3]);
+          s[4] = fmaf(m, R[j][e], s[4]);
+        }
+      }
+    }
+    if (a.w_post != nullptr || a.w_pre != nullptr) row_sum<5>(s, a.tpr, red2, buf2);
+    float r2 = 0.f, k2 = 0.f, k1 = 0.f;
+    if (a.w_pre != nullptr) {
+      r2 = __builtin_amdgcn_rsqf(fmaf(s[0], inv, a.eps));
+      k2 = s[1] * inv * r2 * r2 * r2;
+    }
+    if (a.w_post != nullptr) k1 = (s[2] + fmaf(r2, s[3], -k2 * s[4])) * inv * r1;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float dR[8], dv[8];
       forget(q.dout[j]);
+      forget(q.dres[j]);
+      again(j);
+      if (LEAN && a.w_pre != nullptr) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) R[j][e] = q.res[j].get(e) + scaled(j, e);
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float d = q.dout[j].get(e);
         gpre[j][e] = fmaf(d, R[j][e] * r2, gpre[j][e]);
-        dR[e] = fmaf(r2, fmaf(-k2, R[j][e], d * wpre[j][e]), q.dres[j].get(e));
-      }
-      if (a.dresidual != nullptr) store_pack<RBF16>(a.dresidual, row, c, j, dR);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
+        dR[e] = fmaf(r2, d * wpre[j][e], fmaf(-k2, R[j][e], q.dres[j].get(e)));
         const float dm = (keep[j] >> e) & 1u ? dR[e] * a.keep_scale : 0.f;
         gs[j][e] = fmaf(dm, v[j][e] * r1, gs[j][e]);
-        R[j][e] = dm * w[j][e];
-        s3[0] = fmaf(R[j][e], v[j][e], s3[0]);
+        dv[e] = r1 * fmaf(dm, w[j][e], -k1 * v[j][e]);
       }
-    }
-    float k = 0.f;
-    if (a.w_post != nullptr) {
-      row_sum<1>(s3, a.tpr, red1, buf1);
-      k = s3[0] * inv * r1 * r1;
-    }
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float dv[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) dv[e] = r1 * fmaf(-k, v[j][e], R[j][e]);
+      float dz[8];
       if (a.z != nullptr) {
-        float dz[8];
         forget(q.y[j]);
         forget(q.z[j]);
 #pragma unroll
@@ -391,10 +446,26 @@ __global__ __launch_bounds__(MAXT, WAVES) void norm_bwd_kernel(NormArgs a) {
           dz[e] = dv[e] * q.y[j].get(e) * sg * fmaf(zz, 1.f - sg, 1.f);
           dv[e] *= zz * sg;
         }
-        store_pack<BF16>(a.dz, row, c, j, dz);
       }
-      store_pack<BF16>(a.dy, row, c, j, dv);
+      const int64_t i = row + c.at(j);
+      const Pack<RBF16> pR = Pack<RBF16>::make(dR);
+      const Pack<BF16> pv = Pack<BF16>::make(dv), pz = Pack<BF16>::make(dz);
+      if (c.n(j) >= 8) {
+        if (a.dresidual != nullptr) store_whole<RBF16, false>(a.dresidual, i, pR);
+        store_whole<BF16, false>(a.dy, i, pv);
+        if (a.z != nullptr) store_whole<BF16, false>(a.dz, i, pz);
+      } else {
+        if (a.dresidual != nullptr) store_part<RBF16>(a.dresidual, i, c.n(j), pR);
+        store_part<BF16>(a.dy, i, c.n(j), pv);
+        if (a.z != nullptr) store_part<BF16>(a.dz, i, c.n(j), pz);
+      }
     }
+  };
+  // (a workgroup's rows are walked together: the sums meet at barriers)
+  for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < a.rows; r0 += stride, r += stride) {
+    Row<BF16, RBF16, NV> q = {};
+    q.load(a, start(r), cols_of(r));
+    row_of(r, q);
   }
 
   // rows of the wave, then, where a row is no more than a wave, the waves: one part a workgroup
@@ -432,8 +503,8 @@ __global__ __launch_bounds__(MAXT, WAVES) void norm_bwd_kernel(NormArgs a) {
   const int64_t part = blockIdx.x;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    store_pack<false>(a.ws, part * 2 * a.dim, c, j, gs[j]);
-    store_pack<false>(a.ws, (part * 2 + 1) * a.dim, c, j, gpre[j]);
+    store_pack<false, false>(a.ws, part * 2 * a.dim, c, j, gs[j]);
+    store_pack<false, false>(a.ws, (part * 2 + 1) * a.dim, c, j, gpre[j]);
   }
 }
 
@@ -474,21 +545,21 @@ int threads_per_row(int64_t dim, int NV) {
 }
 int packs_fwd(int64_t dim) { return dim <= 8 * 64 ? 1 : 2; }
 
-// Backward: one pack a thread to 768 threads (three waves a SIMD, 168 registers), in bf16 with the next row's
-// loads ahead; wider rows two packs a thread.
+// Backward: one pack a thread to 768 threads (four waves a SIMD, 128 registers), two to 512, two with the lean
+// form to 1024.  As many workgroups as run at once.  (Five waves a SIMD spill 50 to 70 bytes a lane and cost
+// 40 to 70%.)
 struct BwdShape {
   int NV, tpr, threads;
   int64_t grid;
 };
-constexpr int64_t kAheadDim = 8 * 768;
 BwdShape bwd_shape(int64_t rows, int64_t dim, int num_cus) {
   BwdShape s;
-  s.NV = dim <= kAheadDim ? 1 : 2;
+  s.NV = dim <= 8 * 768 ? 1 : 2;
   s.tpr = threads_per_row(dim, s.NV);
   s.threads = s.tpr <= 64 ? 256 : s.tpr;
   const int rpb = s.threads / s.tpr;
-  const int resident = std::max(1, 12 / (s.threads / 64));   // workgroups of a compute unit
-  s.grid = std::min<int64_t>((int64_t)num_cus * resident, (rows + rpb - 1) / rpb);
+  const int waves = s.NV == 1 ? 16 : s.threads <= 512 ? 8 : 16;   // of a compute unit
+  s.grid = std::min<int64_t>((int64_t)num_cus * std::max(1, waves / (s.threads / 64)), (rows + rpb - 1) / rpb);
   return s;
 }
 
@@ -500,9 +571,9 @@ void pick_fwd(const NormArgs& a, int NV, unsigned grid, int threads, hipStream_t
 template <bool BF16, bool RBF16>
 void pick_bwd(const NormArgs& a, const BwdShape& s, hipStream_t st) {
   const unsigned grid = (unsigned)s.grid;
-  if (s.NV == 1) norm_bwd_kernel<BF16, RBF16, 1, 768, 3, BF16><<<grid, s.threads, 0, st>>>(a);
+  if (s.NV == 1) norm_bwd_kernel<BF16, RBF16, 1, 768, 4, false><<<grid, s.threads, 0, st>>>(a);
   else if (s.threads <= 512) norm_bwd_kernel<BF16, RBF16, 2, 512, 2, false><<<grid, s.threads, 0, st>>>(a);
-  else norm_bwd_kernel<BF16, RBF16, 2, 1024, 4, false><<<grid, s.threads, 0, st>>>(a);
+  else norm_bwd_kernel<BF16, RBF16, 2, 1024, 4, true><<<grid, s.threads, 0, st>>>(a);
 }
 
 }  // namespace
