@@ -449,6 +449,8 @@ size_t ssm_scan_bwd_train_workspace_bytes(int64_t batch, int64_t seqlen, int64_t
  *                 carried-in inputs (of zeros where state_in is NULL)
  * The sums over batch and tokens are taken in a fixed order: the same call
  * gives the same bits.  With batch or seqlen 0, dweight and dbias are zeros.
+ * dx must not overlap x or dout, nor dstate_in the states.  dim up to 2^19 - 1
+ * (SSM_ERR_UNSUPPORTED above).
  * Workspace: ssm_causal_conv1d_bwd_workspace_bytes() (the workgroups' shares
  * of dweight and dbias), or NULL for stream-ordered scratch.
  */
@@ -489,16 +491,17 @@ enum ssm_gated_form {
  *                 states[k] receives the state before token 64k (states[0] is
  *                 h0), for ssm_gated_scan_bwd; ssm_gated_scan_states_bytes()
  *   y           : required; must not overlap an input
- * Workspace: ssm_gated_scan_workspace_bytes() (0 unless few rows of few
- * channels make it split the sequence into chunks that run in parallel), or
- * NULL for stream-ordered scratch.
+ * dim up to 2^21 - 1 (SSM_ERR_UNSUPPORTED above).  The same call gives the same
+ * bits.  Workspace: ssm_gated_scan_workspace_bytes() (two 64-bit words a channel
+ * for every tile of 128 to 2048 tokens; 0 where one tile holds the sequence),
+ * or NULL for stream-ordered scratch; nothing in it needs to be set.
  */
 int ssm_gated_scan_fwd(const void* x, const void* r, const void* i, const float* A, const uint8_t* reset,
                        const float* h0, void* y, float* h_final, float* states,
                        int64_t batch, int64_t seqlen, int64_t dim, int form, int act_dtype,
                        void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace of ssm_gated_scan_fwd.  Depends on the current device. */
+/* Workspace of ssm_gated_scan_fwd. */
 size_t ssm_gated_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int act_dtype);
 
 /* Bytes of states: ceil(seqlen/64) * batch * dim * 4.  0 for empty sizes. */
@@ -529,8 +532,7 @@ int ssm_gated_scan_bwd(const void* x, const void* r, const void* i, const float*
                        int64_t batch, int64_t seqlen, int64_t dim, int form, int act_dtype,
                        void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace of ssm_gated_scan_bwd (have_states: 1 with states, else 0).
- * Depends on the current device. */
+/* Workspace of ssm_gated_scan_bwd (have_states: 1 with states, else 0). */
 size_t ssm_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int act_dtype, int have_states);
 
 /*
@@ -563,7 +565,8 @@ int ssm_gated_state_update(const void* x, const void* r, const void* i, const fl
  * 2011) with key rng[0] and counter (e / 8, rng[1]), 64-bit numbers low word
  * first.  Nothing is stored: the gradient makes the same numbers again.  rng
  * is read on the device when the kernel runs, so a captured graph takes the
- * numbers that are there at each replay.
+ * numbers that are there at each replay.  A dropped element is 0 whatever its
+ * value was (a NaN or infinity there still reaches its row's norm).
  *
  *   y, z, out          : (rows, dim) act dtype
  *   residual, res_out  : (rows, dim) res dtype; res_out (R) may be residual

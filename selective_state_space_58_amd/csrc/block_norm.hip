@@ -15,8 +15,15 @@
 // mask is a function of the element, so the gradient makes it again.
 //
 // Bound by HBM: each input read once, each output written once.  A row is held
-// in the registers of its threads, 8 NV values each; the mean of squares is
-// summed by shuffles and, over several waves, through LDS.
+// in the registers of its threads, 8 NV values each; its sums are taken over
+// lanes by permutations and, over several waves, through LDS.  Measured, bf16
+// with gate, scale and both norms, at a copy's 5.21 TB/s in brackets:
+//   16384 x 5120, fp32 residual, dropout  forward 233 us (226)  backward 425 us (354)
+//   16384 x 1536                          forward  51 us (48)   backward  91 us (77)
+//    8192 x 8192                          forward 127 us (129)  backward 245 us (206)
+//    4096 x 16384                         forward 123 us (129)  backward 425 us (206)
+// The backward's wide rows leave a compute unit one workgroup, whose loads, sums
+// and stores follow each other; above 8192 columns it spills besides.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -431,9 +438,10 @@ __global__ __launch_bounds__(MAXT, WAVES) void norm_bwd_kernel(NormArgs a) {
         const float d = q.dout[j].get(e);
         gpre[j][e] = fmaf(d, R[j][e] * r2, gpre[j][e]);
         dR[e] = fmaf(r2, d * wpre[j][e], fmaf(-k2, R[j][e], q.dres[j].get(e)));
-        const float dm = (keep[j] >> e) & 1u ? dR[e] * a.keep_scale : 0.f;
-        gs[j][e] = fmaf(dm, v[j][e] * r1, gs[j][e]);
-        dv[e] = r1 * fmaf(dm, w[j][e], -k1 * v[j][e]);
+        const bool kept = (keep[j] >> e) & 1u;
+        const float dm = kept ? dR[e] * a.keep_scale : 0.f;
+        gs[j][e] = kept ? fmaf(dm, v[j][e] * r1, gs[j][e]) : gs[j][e];
+        dv[e] = a.w_post != nullptr ? r1 * fmaf(dm, w[j][e], -k1 * v[j][e]) : dm * w[j][e];
       }
       float dz[8];
       if (a.z != nullptr) {
@@ -443,8 +451,9 @@ __global__ __launch_bounds__(MAXT, WAVES) void norm_bwd_kernel(NormArgs a) {
         for (int e = 0; e < 8; ++e) {
           const float zz = q.z[j].get(e);
           const float sg = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-zz * kLog2e));
-          dz[e] = dv[e] * q.y[j].get(e) * sg * fmaf(zz, 1.f - sg, 1.f);
-          dv[e] *= zz * sg;
+          const bool none = a.w_post == nullptr && !((keep[j] >> e) & 1u);   // dropped, whatever y and z are
+          dz[e] = none ? 0.f : dv[e] * q.y[j].get(e) * sg * fmaf(zz, 1.f - sg, 1.f);
+          dv[e] = none ? 0.f : dv[e] * zz * sg;
         }
       }
       const int64_t i = row + c.at(j);
@@ -571,7 +580,7 @@ void pick_fwd(const NormArgs& a, int NV, unsigned grid, int threads, hipStream_t
 template <bool BF16, bool RBF16>
 void pick_bwd(const NormArgs& a, const BwdShape& s, hipStream_t st) {
   const unsigned grid = (unsigned)s.grid;
-  if (s.NV == 1) norm_bwd_kernel<BF16, RBF16, 1, 768, 4, false><<<grid, s.threads, 0, st>>>(a);
+  if (s.NV == 1) norm_bwd_kernel<BF16, RBF16, 1, 768, BF16 || !RBF16 ? 4 : 3, false><<<grid, s.threads, 0, st>>>(a);
   else if (s.threads <= 512) norm_bwd_kernel<BF16, RBF16, 2, 512, 2, false><<<grid, s.threads, 0, st>>>(a);
   else norm_bwd_kernel<BF16, RBF16, 2, 1024, 4, true><<<grid, s.threads, 0, st>>>(a);
 }

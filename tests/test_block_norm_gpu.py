@@ -139,6 +139,20 @@ def test_nan_stays_in_its_row(ssm):
     assert bool(torch.isnan(got["res_out"][2]).all())
 
 
+def test_what_is_dropped_is_not_looked_at(ssm):
+    # without a norm after the block, a NaN or infinity in a dropped place is gone: value and every gradient
+    rows, dim, p = 6, 40, 0.5
+    keep = ref.keep_factors(rows, dim, p, RNG)
+    for parts in ("zrs", "rs", "zrsn"):
+        s, dres, dout = inputs(rows, dim, parts, "f32")
+        s["y"][keep == 0] = 0.0
+        clean = run(ssm, s, dres, dout, p=p)
+        s["y"][keep == 0] = torch.tensor([float("nan"), float("inf")]).repeat(rows * dim)[:int((keep == 0).sum())]
+        got = run(ssm, s, dres, dout, p=p)
+        for k in clean:
+            assert torch.equal(got[k], clean[k]), (parts, k)
+
+
 def test_residual_updated_in_place_and_leading_shapes(ssm):
     s, dres, dout = inputs(6, 40)
     t = {k: v.to(DEV) for k, v in s.items()}
