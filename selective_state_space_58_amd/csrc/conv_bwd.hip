@@ -12,8 +12,8 @@
 // dbias are summed in registers over the run, over a workgroup's runs by
 // shuffles and LDS, and over the workgroups by a second kernel, all in a fixed
 // order.  About 24 vector instructions an element (W = 4, SiLU), four tokens a
-// step with the next step's loads ahead, two channels a thread: 103 registers,
-// four waves a SIMD.  bf16 b8 x 2048 x 1536, W = 4: 33 us and 5 us for the sums
+// step with the next step's loads ahead, two channels a thread: 109 registers,
+// four waves a SIMD.  bf16 b8 x 2048 x 1536, W = 4: 33 us and 4 us for the sums
 // (29 at a copy's rate; four channels a thread and no loads ahead: 40 and 9);
 // b1 x 131072 x 2048: 347 us (309).
 #include <hip/hip_runtime.h>
