@@ -449,7 +449,7 @@ size_t ssm_scan_bwd_train_workspace_bytes(int64_t batch, int64_t seqlen, int64_t
  *                 carried-in inputs (of zeros where state_in is NULL)
  * The sums over batch and tokens are taken in a fixed order: the same call
  * gives the same bits.  With batch or seqlen 0, dweight and dbias are zeros.
- * dx must not overlap x or dout, nor dstate_in the states.  dim up to 2^19 - 1
+ * Outputs must not overlap inputs or each other.  dim up to 2^19 - 1
  * (SSM_ERR_UNSUPPORTED above).
  * Workspace: ssm_causal_conv1d_bwd_workspace_bytes() (the workgroups' shares
  * of dweight and dbias), or NULL for stream-ordered scratch.
@@ -490,11 +490,12 @@ enum ssm_gated_form {
  *   states      : NULL, or, for training, fp32 (ceil(seqlen/64), batch, dim):
  *                 states[k] receives the state before token 64k (states[0] is
  *                 h0), for ssm_gated_scan_bwd; ssm_gated_scan_states_bytes()
- *   y           : required; must not overlap an input
- * dim up to 2^21 - 1 (SSM_ERR_UNSUPPORTED above).  The same call gives the same
- * bits.  Workspace: ssm_gated_scan_workspace_bytes() (two 64-bit words a channel
- * for every tile of 128 to 2048 tokens; 0 where one tile holds the sequence),
- * or NULL for stream-ordered scratch; nothing in it needs to be set.
+ *   y           : required
+ * y, states and h_final must not overlap each other or an input.  dim up to
+ * 2^21 - 1 (SSM_ERR_UNSUPPORTED above).  The same call gives the same bits.
+ * Workspace: ssm_gated_scan_workspace_bytes() (two 64-bit words a channel for
+ * every tile of 128 to 2048 tokens; 0 where one tile holds the sequence), or
+ * NULL for stream-ordered scratch; nothing in it needs to be set.
  */
 int ssm_gated_scan_fwd(const void* x, const void* r, const void* i, const float* A, const uint8_t* reset,
                        const float* h0, void* y, float* h_final, float* states,
@@ -523,7 +524,7 @@ size_t ssm_gated_scan_states_bytes(int64_t batch, int64_t seqlen, int64_t dim);
  *   dx, dr, di: (batch, seqlen, dim) act dtype (di: SSM_GATED_LRU only, else ignored)
  *   dA        : (dim) fp32, SSM_GATED_LRU only, else ignored; summed in a fixed order
  *   dh0       : (batch, dim) fp32 or NULL
- * Outputs must not overlap inputs.  Workspace:
+ * Outputs must not overlap inputs or each other.  Workspace:
  * ssm_gated_scan_bwd_workspace_bytes(), or NULL for stream-ordered scratch.
  */
 int ssm_gated_scan_bwd(const void* x, const void* r, const void* i, const float* A, const uint8_t* reset,
@@ -541,8 +542,8 @@ size_t ssm_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t
  *   x, r, i, y : (batch, dim) act dtype (i: SSM_GATED_LRU only, else NULL)
  *   A          : (dim) fp32; SSM_GATED_LRU only, else NULL
  *   state      : (batch, dim) fp32 (required)
- *   y          : required; must not overlap the state or an input
- * No workspace.
+ *   y          : required
+ * y and the state must not overlap each other or an input.  No workspace.
  */
 int ssm_gated_state_update(const void* x, const void* r, const void* i, const float* A, float* state, void* y,
                            int64_t batch, int64_t dim, int form, int act_dtype, void* stream);
@@ -592,7 +593,7 @@ int ssm_block_norm_fwd(const void* y, const void* z, const void* residual, const
  *   dz, dresidual, dw_post, dscale, dw_pre : required when z, residual,
  *                w_post, scale, w_pre are given, else ignored; the last three
  *                (dim) fp32, summed over the rows in a fixed order
- * Outputs must not overlap inputs.  Workspace:
+ * Outputs must not overlap inputs or each other.  Workspace:
  * ssm_block_norm_bwd_workspace_bytes(), or NULL for stream-ordered scratch.
  */
 int ssm_block_norm_bwd(const void* y, const void* z, const void* residual, const float* w_post, const float* scale,

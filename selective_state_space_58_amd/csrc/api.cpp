@@ -40,6 +40,18 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const char *p = (const char*)a, *q = (const char*)b;
   return p != nullptr && q != nullptr && na > 0 && nb > 0 && p < q + nb && q < p + na;
 }
+struct Span { const void* p; size_t bytes; };
+// Whether an output shares memory with another or with an input.
+template <size_t NO, size_t NI>
+bool clash(const Span (&out)[NO], const Span (&in)[NI]) {
+  for (size_t o = 0; o < NO; ++o) {
+    for (const Span& q : in)
+      if (overlap(out[o].p, out[o].bytes, q.p, q.bytes)) return true;
+    for (size_t k = 0; k < o; ++k)
+      if (overlap(out[o].p, out[o].bytes, out[k].p, out[k].bytes)) return true;
+  }
+  return false;
+}
 
 // Stream-ordered scratch for calls that pass no workspace.
 struct Scratch {
@@ -620,8 +632,11 @@ int ssm_gated_scan_fwd(const void* x, const void* r, const void* i, const float*
     return fail(SSM_ERR_ALIGNMENT, "a pointer is not aligned to its element size");
   if (batch == 0 || dim == 0) return SSM_OK;
   const size_t n = (size_t)(batch * seqlen * dim) * as;
-  if (overlap(y, n, x, n) || overlap(y, n, r, n) || overlap(y, n, i, n))
-    return fail(SSM_ERR_SHAPE, "y must not overlap an input");
+  const size_t nd = (size_t)dim * 4, nh = (size_t)batch * nd, ns = (size_t)((seqlen + 63) / 64) * nh;
+  const Span in[] = {{x, n}, {r, n}, {i, n}, {A, nd}, {reset, (size_t)(batch * seqlen)}};
+  const Span out[] = {{y, n}, {states, ns}, {h_final, nh}};
+  if (clash(out, in) || overlap(y, n, h0, nh) || overlap(states, ns, h0, nh) || (h_final != h0 && overlap(h_final, nh, h0, nh)))
+    return fail(SSM_ERR_SHAPE, "y, states and h_final must not overlap each other or an input (h_final may be h0)");
   const bool vec = dim % 2 == 0 && aligned(x, 2 * as) && aligned(r, 2 * as) && aligned(i, 2 * as) && aligned(y, 2 * as);
   const GatedPlan p = plan_gated(batch, seqlen, dim, act_dtype == SSM_BF16, vec, false);
   Scratch own;
@@ -686,8 +701,8 @@ int ssm_gated_state_update(const void* x, const void* r, const void* i, const fl
     return fail(SSM_ERR_ALIGNMENT, "a pointer is not aligned to its element size");
   if (!has) return SSM_OK;
   const size_t n = (size_t)(batch * dim) * as, ns = (size_t)(batch * dim) * 4;
-  if (overlap(y, n, state, ns) || overlap(y, n, x, n) || overlap(y, n, r, n) || overlap(y, n, i, n))
-    return fail(SSM_ERR_SHAPE, "y must not overlap the state or an input");
+  const Span in[] = {{x, n}, {r, n}, {i, n}, {A, (size_t)dim * 4}}, out[] = {{y, n}, {state, ns}};
+  if (clash(out, in)) return fail(SSM_ERR_SHAPE, "y and the state must not overlap each other or an input");
   GatedArgs a{};
   a.x = x; a.r = r; a.i = i; a.A = A; a.states = state; a.y = y;
   a.batch = batch; a.dim = dim; a.seqlen = 1; a.form = form; a.act_bf16 = act_dtype == SSM_BF16;

@@ -28,6 +28,23 @@ def test_gated_fwd_refusals(kw, code):
     assert lib.ssm_last_error() != b""
 
 
+S = Q + 0x1000000   # and one output from the other
+
+
+@pytest.mark.parametrize("kw", [
+    dict(st=Q), dict(st=P), dict(st=S, hf=S), dict(st=S, h0=S), dict(hf=Q), dict(hf=P), dict(hf=Q + 116), dict(h0=Q),
+    dict(st=S, hf=S + 44), dict(reset=Q), dict(reset=S, st=S), dict(A=Q), dict(A=S, hf=S),
+])
+def test_gated_fwd_refuses_buffers_that_share_memory(kw):
+    # 2 x 5 x 6: y is 120 bytes, h0, h_final and states (one row of states) 48, A 24, reset 10
+    assert gated_fwd(_lib(), **kw) == 2
+
+
+@pytest.mark.parametrize("kw", [dict(state=P), dict(x=Q + 4), dict(A=Q), dict(A=Q + 0x100000), dict(r=Q + 44), dict(i=Q)])
+def test_gated_step_refuses_buffers_that_share_memory(kw):
+    assert step(_lib(), **kw) == 2
+
+
 def gated_bwd(lib, **kw):
     a = dict(x=P, r=P, i=P, A=P, reset=None, h0=None, st=P, dout=P, dhf=None, dx=Q, dr=Q, di=Q, dA=Q, dh0=None, batch=2,
              seqlen=5, dim=6, form=0, act=1, ws=None, wsb=0)
