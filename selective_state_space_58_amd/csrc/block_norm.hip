@@ -21,9 +21,10 @@
 //   16384 x 5120, fp32 residual, dropout  forward 233 us (226)  backward 425 us (354)
 //   16384 x 1536                          forward  51 us (48)   backward  91 us (77)
 //    8192 x 8192                          forward 127 us (129)  backward 245 us (206)
-//    4096 x 16384                         forward 123 us (129)  backward 425 us (206)
+//    4096 x 16384                         forward 123 us (129)  backward 358 us (206)
 // The backward's wide rows leave a compute unit one workgroup, whose loads, sums
-// and stores follow each other; above 8192 columns it spills besides.
+// and stores follow each other; above 8192 columns it reads the weights twice for
+// every row and spills 64 bytes a lane besides.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -284,8 +285,9 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs a) {
 // two rounds of sums over a row, sum v^2 and then five at once.
 // A workgroup walks rows that lie gridDim.x apart and keeps its share of S and
 // dw_pre in registers.  LEAN, for rows that leave a thread 128 registers for two
-// packs: the weights are read again where they are used, and v and R formed again
-// for the gradients.  (The next row's loads ahead of the sums: no gain where the
+// packs: the share lies in LDS, the weights are read again where they are used, and
+// v and R formed again for the gradients.  (The share in registers: 513 us against
+// 358 on 4096 x 16384; four packs for half the threads, at 256 registers: 376.  The next row's loads ahead of the sums: no gain where the
 // packs' loads stand in one branch, 425 against 422 us on 16384 x 5120.)
 template <bool BF16, bool RBF16, int NV>
 struct Row {
@@ -327,7 +329,29 @@ __global__ __launch_bounds__(MAXT, WAVES) void norm_bwd_kernel(NormArgs a) {
   const int tid = threadIdx.x % a.tpr;
   const float inv = 1.f / (float)a.dim;
   int buf1 = 0, buf2 = 0;
+  // this thread's share of S and dw_pre; LEAN keeps it in LDS, four channels a thread in turn, as only it reads it
   float gs[NV][8], gpre[NV][8];
+  __shared__ float4 share[LEAN ? 2 * NV * 2 : 1][LEAN ? MAXT : 1];
+  auto from_share = [&](int j) {
+    if constexpr (LEAN) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float4 s = share[j * 4 + k][threadIdx.x], p = share[j * 4 + 2 + k][threadIdx.x];
+        gs[j][4 * k] = s.x; gs[j][4 * k + 1] = s.y; gs[j][4 * k + 2] = s.z; gs[j][4 * k + 3] = s.w;
+        gpre[j][4 * k] = p.x; gpre[j][4 * k + 1] = p.y; gpre[j][4 * k + 2] = p.z; gpre[j][4 * k + 3] = p.w;
+      }
+    }
+  };
+  auto to_share = [&](int j) {
+    if constexpr (LEAN) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        share[j * 4 + k][threadIdx.x] = make_float4(gs[j][4 * k], gs[j][4 * k + 1], gs[j][4 * k + 2], gs[j][4 * k + 3]);
+        share[j * 4 + 2 + k][threadIdx.x] =
+            make_float4(gpre[j][4 * k], gpre[j][4 * k + 1], gpre[j][4 * k + 2], gpre[j][4 * k + 3]);
+      }
+    }
+  };
   // w and w_pre of a thread's pack j
   auto weights = [&](int j, float (&w)[8], float (&wpre)[8]) {
     const Cols c{tid, a.tpr, (int)a.dim};
@@ -351,6 +375,7 @@ __global__ __launch_bounds__(MAXT, WAVES) void norm_bwd_kernel(NormArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) gs[j][e] = gpre[j][e] = 0.f;
     if (!LEAN) weights(j, w[j], wpre[j]);
+    to_share(j);
   }
 
   const int64_t stride = (int64_t)gridDim.x * rpb;
@@ -429,6 +454,7 @@ __global__ __launch_bounds__(MAXT, WAVES) void norm_bwd_kernel(NormArgs a) {
       forget(q.dout[j]);
       forget(q.dres[j]);
       again(j);
+      from_share(j);
       if (LEAN && a.w_pre != nullptr) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) R[j][e] = q.res[j].get(e) + scaled(j, e);
@@ -443,6 +469,7 @@ __global__ __launch_bounds__(MAXT, WAVES) void norm_bwd_kernel(NormArgs a) {
         gs[j][e] = kept ? fmaf(dm, v[j][e] * r1, gs[j][e]) : gs[j][e];
         dv[e] = a.w_post != nullptr ? r1 * fmaf(dm, w[j][e], -k1 * v[j][e]) : dm * w[j][e];
       }
+      to_share(j);
       float dz[8];
       if (a.z != nullptr) {
         forget(q.y[j]);
@@ -477,6 +504,8 @@ __global__ __launch_bounds__(MAXT, WAVES) void norm_bwd_kernel(NormArgs a) {
     row_of(r, q);
   }
 
+#pragma unroll
+  for (int j = 0; j < NV; ++j) from_share(j);
   // rows of the wave, then, where a row is no more than a wave, the waves: one part a workgroup
   for (int sh = a.tpr; sh < 64; sh <<= 1)
 #pragma unroll
